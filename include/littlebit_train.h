@@ -1,0 +1,91 @@
+/*
+ * littlebit_train.h -- C ABI of the operators around the LittleBit layers in
+ * quantisation-aware training (B200, sm_100a).
+ *
+ * littlebit_backward.h carries gradients through a layer; a training step also
+ * needs both ends of the model and an update of the latent factors:
+ *   - the token embedding and its gradient,
+ *   - the softmax cross entropy of the last hidden states against the
+ *     vocabulary matrix, with the gradients of both,
+ *   - the orthogonalised update of a latent factor (the Newton-Schulz form of
+ *     the Muon optimiser) from its gradient dU or dV.
+ *
+ * Conventions are those of littlebit.h: device pointers unless stated, arrays
+ * of pointers are HOST arrays of device pointers, row-major dense matrices,
+ * `stream` is a cudaStream_t passed as void*, every check is made before
+ * anything is enqueued, nothing synchronises the host unless it says so.  No
+ * call here allocates device memory or keeps anything between calls: scratch
+ * is the `workspace` argument, 256-byte aligned and at least as large as the
+ * matching *_workspace_bytes call says; its contents need not be initialised
+ * and mean nothing afterwards.  Calls that use different workspaces and
+ * outputs may overlap on the device (streams, captured graphs); calls that
+ * share one must be ordered.  All calls can be captured into a CUDA graph.
+ * Outputs must not overlap inputs.  Results are the same bits in every run.
+ */
+#ifndef LITTLEBIT_TRAIN_H
+#define LITTLEBIT_TRAIN_H
+
+#include "littlebit.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of the operators that take more than one. */
+typedef enum lb_dtype {
+    LB_F32 = 0,   /* IEEE binary32 */
+    LB_BF16 = 1   /* bfloat16      */
+} lb_dtype;
+
+/*
+ * Softmax cross entropy against a vocabulary matrix, without the logits:
+ *     z = H W^T [M x V],  lse_m = log sum_v exp z_mv,  loss_m = lse_m - z_m,label(m)
+ *
+ *   H       bfloat16 [M][D], hidden states        W       bfloat16 [V][D], vocabulary matrix
+ *   labels  int64 [M]; a label outside 0 .. V-1 (such as -100) marks a row that does not count: its loss is 0
+ *   loss    float32 [M]                           lse     float32 [M] (every row)
+ * H and W 16-byte aligned, D a multiple of 8, D, V >= 1; M = 0 is a valid
+ * empty call.  Products accumulate in float32 on the tensor cores; the maximum
+ * and sum of the softmax are float32.  A row with a NaN or an infinite logit
+ * has lse and loss NaN (an infinity below every other logit counts as weight 0).
+ * Errors: LB_ERR_INVALID_ARG (null, misaligned, bad size, workspace too
+ * small), LB_ERR_UNSUPPORTED (D not a multiple of 8, sizes past 2^30 rows or
+ * tiles), LB_ERR_CUDA.
+ */
+LB_API size_t lb_cross_entropy_forward_workspace_bytes(int M, int D, int V);
+LB_API lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t *W, const int64_t *labels, int M, int D,
+                                          int V, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                          void *stream);
+
+/*
+ * The same loss together with its gradients, for row weights w (the derivative
+ * of the training objective by each row's loss, 1 / count for a mean):
+ *     G = diag(w) (softmax(z) - onehot(labels)),   dH = G W,   dW = G^T H
+ * A row that does not count has G = 0, whatever its hidden state holds.
+ *
+ *   weight  float32 [M]       loss  float32 [M]
+ *   dH      bfloat16 [M][D]   dW    bfloat16 [V][D], or NULL for a frozen vocabulary matrix; both are overwritten
+ *   rows    rows taken at a time (0: 8192; at most 32768).  The scratch holds 16 bits per
+ *           logit of one such piece, never of all M rows when M is larger;
+ *           with more than one piece dW is summed over them in float32.
+ * G is rounded to bfloat16 once, as an operand of the two products; they
+ * accumulate in float32 and dH, dW are rounded once.  All else as above; rows
+ * must be >= 0; with M = 0 only dW is written (zeros).
+ */
+LB_API size_t lb_cross_entropy_gradient_workspace_bytes(int M, int D, int V, int with_dW, int rows);
+LB_API lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W, const int64_t *labels,
+                                           const float *weight, int M, int D, int V, int rows, float *loss,
+                                           uint16_t *dH, uint16_t *dW, void *workspace, size_t workspace_bytes,
+                                           void *stream);
+
+/* Device-side status of the tensor-core kernels of this header on the current
+ * device: synchronises `stream`, returns LB_ERR_TIMEOUT if a bounded wait gave
+ * up since the last check (the outputs of that call are unspecified) and
+ * clears it.  Not to be called while a stream is being captured. */
+LB_API lb_status lb_train_status(void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LITTLEBIT_TRAIN_H */

@@ -1,0 +1,562 @@
+// Softmax cross entropy of hidden states H [M][D] against a vocabulary matrix
+// W [V][D], with the gradients of both, without keeping the logits.
+//
+//     z = H W^T,  lse = log sum_v exp z_v,  loss = lse - z_label
+//     G = w (softmax(z) - onehot),  dH = G W,  dW = G^T H
+//
+// Floor: 2 M V D flops for the loss and 6 M V D with both gradients (H and W
+// are read once from memory: at the sizes of a training step the tensor cores
+// bound all three products).  So every logit is computed once:
+//
+//   1  z tiles (256 rows x 256 vocabulary entries) on CTA pairs.  The epilogue
+//      takes each row's maximum m and sum of exp(z - m) over the tile (one
+//      thread a row, two passes over tensor memory) and, for the gradient,
+//      leaves e = 2^15 exp(z - m) in binary16: at most 2^15, exact to 2^-12
+//      down to 2^-29 of the tile's maximum and to 2^-39 of it below that.
+//   2  one block per row and 8192 entries: lse from the tiles' (m, s), then
+//      G = w (e exp(m - lse) 2^-15 - onehot) rounded to bfloat16 over e.
+//   3  dH = G W and dW = G^T H in one launch; G and W (dH) and G and H (dW)
+//      are read in the orientation they are stored in, whichever index is
+//      contracted.
+//
+// Keeping e costs 2 bytes a logit of one piece of rows, written, turned into G
+// and read twice; recomputing z instead would cost a third more flops.
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "lb_mm.cuh"
+#include "littlebit_train.h"
+
+namespace lb {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kEScale = 15.0f;        // e is stored times 2^15
+constexpr int kGradCols = 8192;         // entries of a row one block of the second step takes
+constexpr int kRowsDefault = 8192, kRowsMost = 32768;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// value where at == i, else `other`; opaque, so that a loop of them is not turned into an indexed copy of the registers
+__device__ __forceinline__ uint32_t pick(int at, int i, uint32_t value, uint32_t other)
+{
+    uint32_t r;
+    asm("{\n.reg .pred p;\nsetp.eq.s32 p, %1, %2;\nselp.b32 %0, %3, %4, p;\n}\n"
+        : "=r"(r)
+        : "r"(at), "r"(i), "r"(value), "r"(other));
+    return r;
+}
+
+// Before the staging block is written again, its last copy must have been read.
+__device__ __forceinline__ void staging_free(bool &stored, int lane)
+{
+    if (stored) {
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+    }
+    stored = true;
+}
+
+// ---- 1: statistics of a tile of logits (kKeep: and e)
+template <bool kKeep>
+struct LogitEpi {
+    struct Params {
+        CUtensorMap mE;            // binary16 [rows][Vp]
+        const int64_t *labels;
+        float2 *stat;              // [rows][ntn]: (reference exponent, sum), base 2
+        float *target;             // [rows]: z of the label
+        int M, V, ntn;
+    };
+    static __device__ __forceinline__ void run(const Params &E, const MmBatch<1> &, const MmUnit &U, const MmTileCtx &T,
+                                               bool &stored)
+    {
+        const int row = T.row0 + T.lane;
+        const int valid = min(kMmTile, E.V - T.col0);   // columns of the tile inside the vocabulary
+        if (T.row0 >= E.M) return;
+        long long lab = row < E.M ? E.labels[row] : -1;
+        const int at = lab >= T.col0 && lab < T.col0 + valid ? (int)(lab - T.col0) : -1;
+        float mx = -INFINITY;
+        uint32_t v[32];
+        for (int c = 0; c < valid; c += 32) {
+            tmem_ld32(T.tmem + c, v);
+            if (c + 32 > valid) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i >= valid) v[i] = 0xff800000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+            if (at >= c && at < c + 32) {
+                uint32_t z = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z = pick(at - c, i, v[i], z);
+                E.target[row] = __uint_as_float(z);
+            }
+        }
+        const float ref = fmaf(mx, kLog2e, -kEScale);
+        const float sub = mx == -INFINITY ? 0.0f : ref;   // a tile of nothing but -inf (or NaN): weights 0 (or NaN)
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int cols = kKeep ? (valid + 63) & ~63 : (valid + 31) & ~31;
+        for (int c = 0; c < cols; c += 32) {
+            tmem_ld32(T.tmem + c, v);
+            if (c + 32 > valid) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i >= valid) v[i] = 0xff800000u;
+            }
+            float e[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                e[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -sub));
+                s[i & 3] += e[i];
+            }
+            if (kKeep) {
+                const int half = (c >> 5) & 1;   // 32 columns = half of a 128-byte staging row
+                if (half == 0) staging_free(stored, T.lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sts128(T.st + sw128(T.lane, half * 4 + i),
+                           make_uint4(pack_h2(e[8 * i], e[8 * i + 1]), pack_h2(e[8 * i + 2], e[8 * i + 3]),
+                                      pack_h2(e[8 * i + 4], e[8 * i + 5]), pack_h2(e[8 * i + 6], e[8 * i + 7])));
+                if (half == 1) {
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (T.lane == 0) tma_store_2d(&E.mE, T.col0 + c - 32, T.row0, T.st);
+                }
+            }
+        }
+        if (row < E.M) E.stat[(size_t)row * E.ntn + U.tn] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
+    }
+};
+
+// ---- lse (base 2) of a row from its tiles' statistics, by a group of kThreads threads (a warp, or a block)
+__device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
+{
+    // (m, s): sum of s 2^m.  NaN in either sum stays; an empty side (-inf, 0) adds nothing.
+    const float m = fmaxf(a.x, b.x);
+    if (m == -INFINITY) return make_float2(m, a.y + b.y);
+    return make_float2(m, a.y * ex2(a.x - m) + b.y * ex2(b.x - m));
+}
+
+__device__ __forceinline__ float2 lse_warp(float2 a)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float2 b = make_float2(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o));
+        a = lse_merge(a, b);
+    }
+    return a;
+}
+
+__global__ void __launch_bounds__(256) lse_kernel(const float2 *__restrict__ stat, const float *__restrict__ target,
+                                                  const int64_t *__restrict__ labels, int M, int V, int ntn,
+                                                  float *__restrict__ loss, float *__restrict__ lse)
+{
+    const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= M) return;
+    float2 a = make_float2(-INFINITY, 0.0f);
+    for (int t = lane; t < ntn; t += 32) a = lse_merge(a, stat[(size_t)row * ntn + t]);
+    a = lse_warp(a);
+    if (lane == 0) {
+        const long long lab = labels[row];
+        const float l = (a.x + log2f(a.y)) * kLn2;
+        lse[row] = l;
+        loss[row] = lab >= 0 && lab < V ? l - target[row] : 0.0f;
+    }
+}
+
+// ---- 2: G over e, the loss, and (Hc) H with the rows that do not count zeroed, the operand of dW
+__global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const float2 *__restrict__ stat,
+                                                   const float *__restrict__ target,
+                                                   const int64_t *__restrict__ labels,
+                                                   const float *__restrict__ weight, int V, int Vp, int ntn, int D,
+                                                   const uint4 *__restrict__ H, uint4 *__restrict__ Hc,
+                                                   float *__restrict__ loss)
+{
+    const int row = blockIdx.y, chunk = blockIdx.x;
+    const long long lab = labels[row];
+    const bool counts = lab >= 0 && lab < V;
+    if (chunk == 0 && Hc) {
+        const int nv = D / 8;
+        const size_t base = (size_t)row * nv;
+        for (int i = threadIdx.x; i < nv; i += 256) Hc[base + i] = counts ? H[base + i] : make_uint4(0, 0, 0, 0);
+    }
+    const int v0 = chunk * (kGradCols / 8), v1 = min(Vp / 8, v0 + kGradCols / 8);   // vectors of 8 entries
+    uint4 *out = E + (size_t)row * (Vp / 8);
+    if (!counts) {
+        for (int i = v0 + threadIdx.x; i < v1; i += 256) out[i] = make_uint4(0, 0, 0, 0);
+        if (chunk == 0 && threadIdx.x == 0) loss[row] = 0.0f;
+        return;
+    }
+    const float2 *st = stat + (size_t)row * ntn;
+    float2 a = make_float2(-INFINITY, 0.0f);
+    for (int t = threadIdx.x; t < ntn; t += 256) a = lse_merge(a, st[t]);
+    a = lse_warp(a);
+    __shared__ float2 part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = lse_warp(part[threadIdx.x & 7]);   // every warp: the eight parts, four times over
+    a.y *= 0.25f;
+    const float lse2 = a.x + log2f(a.y);
+    const float w = weight[row];
+    if (chunk == 0 && threadIdx.x == 0) loss[row] = lse2 * kLn2 - target[row];
+#pragma unroll 4
+    for (int i = v0 + threadIdx.x; i < v1; i += 256) {
+        const uint4 q = out[i];
+        const float f = w * ex2(st[i >> 5].x - lse2);   // 32 vectors to a tile of 256 entries
+        const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 e = __half22float2(*reinterpret_cast<const __half2 *>(&in[j]));
+            g[2 * j] = e.x * f;
+            g[2 * j + 1] = e.y * f;
+        }
+        if (lab >> 3 == i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if ((lab & 7) == j) g[j] -= w;
+        }
+        out[i] = make_uint4(pack_bf2(g[0], g[1]), pack_bf2(g[2], g[3]), pack_bf2(g[4], g[5]), pack_bf2(g[6], g[7]));
+    }
+}
+
+// ---- 3: the two products
+enum { kOutBf16 = 0, kOutF32 = 1, kOutF32Add = 2 };
+struct ProductEpi {
+    struct Params {
+        CUtensorMap mD[2];
+        int kind[2];
+        int split_rows[2];   // rows between the partial results of consecutive k ranges
+    };
+    static __device__ __forceinline__ void run(const Params &E, const MmBatch<2> &G, const MmUnit &U, const MmTileCtx &T,
+                                               bool &stored)
+    {
+        const MmProb &P = G.p[U.q];
+        if (T.row0 >= P.M) return;
+        const int kind = E.kind[U.q], y = T.row0 + U.split * E.split_rows[U.q];
+        const CUtensorMap *map = &E.mD[U.q];
+        const int cols = min(kMmTile, P.N - T.col0);
+        uint32_t v[32];
+        for (int c = 0; c < cols; c += 32) {
+            tmem_ld32(T.tmem + c, v);
+            if (kind == kOutBf16) {
+                const int half = (c >> 5) & 1;
+                if (half == 0) staging_free(stored, T.lane);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        p[j] = pack_bf2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                    sts128(T.st + sw128(T.lane, half * 4 + i), make_uint4(p[0], p[1], p[2], p[3]));
+                }
+                if (half == 0 && c + 32 < cols) continue;
+                fence_proxy_async();
+                __syncwarp();
+                if (T.lane == 0) tma_store_2d(map, T.col0 + (c & ~63), y, T.st);
+            } else {
+                staging_free(stored, T.lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sts128(T.st + sw128(T.lane, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                fence_proxy_async();
+                __syncwarp();
+                if (T.lane == 0) {
+                    if (kind == kOutF32)
+                        tma_store_2d(map, T.col0 + c, y, T.st);
+                    else
+                        tma_add_2d(map, T.col0 + c, y, T.st);
+                }
+            }
+        }
+    }
+};
+
+// out = bfloat16(sum of n fp32 parts `stride` elements apart), in order; 8 elements a thread
+__global__ void __launch_bounds__(256) round_sum_kernel(const float4 *__restrict__ part, size_t stride4, int n,
+                                                        size_t nvec, uint4 *__restrict__ out)
+{
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nvec; i += (size_t)gridDim.x * 256) {
+        float4 a = part[2 * i], b = part[2 * i + 1];
+        for (int s = 1; s < n; ++s) {
+            const float4 c = part[s * stride4 + 2 * i], d = part[s * stride4 + 2 * i + 1];
+            a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+            b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+        }
+        out[i] = make_uint4(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w), pack_bf2(b.x, b.y), pack_bf2(b.z, b.w));
+    }
+}
+
+// ---- host
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// K ranges of dH: k is the whole vocabulary, so a few rows give few, long tiles.  The time of `s` ranges in 64-deep k
+// blocks of a pair (0.41 us): the launch's longest chain, plus the write and read of the fp32 partial results at the
+// copy rate (2.7 MB in that time), which one range does not need.  Measured at M = 16, D = 8192, V = 32000 (frozen W).
+int dh_splits(int M, int D, int V, bool with_dW, int pairs)
+{
+    const long tiles = (long)((M + kMmTile - 1) / kMmTile) * ((D + kMmTile - 1) / kMmTile);
+    const long nkb = ((long)V + kMmBK - 1) / kMmBK;
+    const long dw_len = (M + kMmBK - 1) / kMmBK;
+    const double dw = with_dW ? (double)((V + kMmTile - 1) / kMmTile) * ((D + kMmTile - 1) / kMmTile) * dw_len : 0.0;
+    int best = 1;
+    double best_cost = 1e300;
+    for (int s = 1; s <= 16 && s <= nkb; ++s) {
+        const long len = (nkb + s - 1) / s, units = tiles * s;
+        const double chain = (double)((units + pairs - 1) / pairs) * len;
+        const double even = ((double)units * len + dw) / pairs + (with_dW ? dw_len : 0);
+        const double cost = std::max(chain, even) + (s > 1 ? 8.0 + (double)s * M * D * 8.0 / 2.7e6 : 0.0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+struct LossPlan {
+    int rows, npieces, ntn, Vp, splits;
+    size_t stat, target, E, Hc, part, acc, bytes;   // workspace offsets
+};
+
+bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int rows)
+{
+    if (M < 0 || D < 1 || V < 1 || rows < 0 || D > (1 << 20) || V > (1 << 28) || M > (1 << 28)) return false;
+    memset(&L, 0, sizeof(L));
+    L.rows = std::min(std::max(M, 1), grad ? (rows ? std::min(rows, kRowsMost) : kRowsDefault) : std::max(M, 1));
+    L.npieces = M ? (M + L.rows - 1) / L.rows : 0;
+    L.ntn = (V + kMmTile - 1) / kMmTile;
+    L.Vp = (V + 7) & ~7;
+    size_t at = 0;
+    auto take = [&](size_t b) {
+        const size_t o = at;
+        at = up256(at + b);
+        return o;
+    };
+    L.stat = take((size_t)L.rows * L.ntn * sizeof(float2));
+    L.target = take((size_t)L.rows * 4);
+    if (grad) {
+        // the plan's pairs: those of the B200's 148 SMs, whatever the current device, so that the size is one number
+        L.splits = dh_splits(L.rows, D, V, with_dW, 74);
+        L.E = take((size_t)L.rows * L.Vp * 2);
+        const size_t tile_rows = (size_t)((L.rows + kMmTile - 1) / kMmTile) * kMmTile;
+        L.part = take(L.splits > 1 ? (size_t)L.splits * tile_rows * D * 4 : 0);
+        L.Hc = take(with_dW ? (size_t)L.rows * D * 2 : 0);
+        L.acc = take(with_dW && L.npieces > 1 ? (size_t)V * D * 4 : 0);
+    }
+    L.bytes = at;
+    return true;
+}
+
+bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const int64_t *labels, int M, int D, int V,
+                 unsigned char *ws, bool keep, cudaStream_t s)
+{
+    MmBatch<1> G;
+    memset(&G, 0, sizeof(G));
+    G.n = 1;
+    mm_plan(G.p[0], M, V, D, 1, true, 0, 1);
+    G.nunits = mm_units(G.p[0]);
+    if (!mm_operand(&G.p[0].mA, true, false, H, M, D, D) || !mm_operand(&G.p[0].mB, true, false, W, V, D, D))
+        return LB_ERR_INVALID_ARG;
+    auto fill = [&](auto &E) {
+        memset(&E, 0, sizeof(E));
+        E.labels = labels;
+        E.stat = (float2 *)(ws + L.stat);
+        E.target = (float *)(ws + L.target);
+        E.M = M;
+        E.V = V;
+        E.ntn = L.ntn;
+    };
+    if (keep) {
+        LogitEpi<true>::Params E;
+        fill(E);
+        if (!tmap_encode_2d(&E.mE, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + L.E, L.Vp, M, (long)L.Vp * 2, 64, 32))
+            return LB_ERR_INVALID_ARG;
+        return status_from(mm_launch<true, 1, LogitEpi<true>>(G, E, s));
+    }
+    LogitEpi<false>::Params E;
+    fill(E);
+    return status_from(mm_launch<true, 1, LogitEpi<false>>(G, E, s));
+}
+
+// dH (and dW) of one piece of M rows
+lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, uint16_t *dH, uint16_t *dW, bool first,
+                   unsigned char *ws, cudaStream_t s, int *launches)
+{
+    MmBatch<2> G;
+    ProductEpi::Params E;
+    memset(&G, 0, sizeof(G));
+    memset(&E, 0, sizeof(E));
+    const void *Gm = ws + L.E;
+    MmProb &P = G.p[0];
+    mm_plan(P, M, D, V, 1, true, 0, L.splits);
+    P.b_mn = 1;
+    if (!mm_operand(&P.mA, true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&P.mB, true, true, W, V, D, D))
+        return LB_ERR_INVALID_ARG;
+    const int tile_rows = P.ntm * kMmTile;
+    bool ok;
+    if (P.splits > 1) {
+        E.kind[0] = kOutF32;
+        E.split_rows[0] = tile_rows;
+        ok = tmap_encode_2d(&E.mD[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.part, D, (long)tile_rows * P.splits,
+                            (long)D * 4, 32, 32);
+    } else {
+        E.kind[0] = kOutBf16;
+        ok = tmap_encode_2d(&E.mD[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dH, D, M, (long)D * 2, 64, 32);
+    }
+    if (!ok) return LB_ERR_INVALID_ARG;
+    G.n = 1;
+    G.nunits = mm_units(P);
+    if (dW) {
+        MmProb &Q = G.p[1];
+        mm_plan(Q, V, D, M, 1, false, G.nunits, 1);
+        Q.a_mn = Q.b_mn = 1;
+        if (!mm_operand(&Q.mA, true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&Q.mB, true, true, ws + L.Hc, M, D, D))
+            return LB_ERR_INVALID_ARG;
+        if (L.npieces > 1) {
+            E.kind[1] = first ? kOutF32 : kOutF32Add;
+            ok = tmap_encode_2d(&E.mD[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.acc, D, V, (long)D * 4, 32, 32);
+        } else {
+            E.kind[1] = kOutBf16;
+            ok = tmap_encode_2d(&E.mD[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, D, V, (long)D * 2, 64, 32);
+        }
+        if (!ok) return LB_ERR_INVALID_ARG;
+        int pairs = 0;
+        const cudaError_t e = mm_pairs(&pairs);
+        if (e != cudaSuccess) return status_from(e);
+        const int n1 = mm_units(Q), more = G.nunits % pairs;
+        if (more) G.extra = (int)std::min<long>((P.kb_per + Q.kb_per / 2) / Q.kb_per, n1 / (pairs - more));
+        G.n = 2;
+        G.nunits += n1;
+        if (pairs > G.nunits) G.extra = 0;   // fewer pairs are launched than the rule above counted with
+    }
+    const cudaError_t e = mm_launch<true, 2, ProductEpi>(G, E, s);
+    if (e != cudaSuccess) return status_from(e);
+    ++*launches;
+    if (P.splits > 1) {
+        const size_t nvec = (size_t)M * D / 8;
+        const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
+        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.part), (size_t)tile_rows * D / 4, P.splits, nvec,
+                                              (uint4 *)dH);
+        ++*launches;
+    }
+    return status_from(cudaGetLastError());
+}
+
+}  // namespace
+
+lb_status loss_status(cudaStream_t s) { return mm_status(s); }
+
+}  // namespace lb
+
+using namespace lb;
+
+extern "C" size_t lb_cross_entropy_forward_workspace_bytes(int M, int D, int V)
+{
+    LossPlan L;
+    return loss_plan(L, M, D, V, false, false, 0) ? L.bytes : 0;
+}
+
+extern "C" size_t lb_cross_entropy_gradient_workspace_bytes(int M, int D, int V, int with_dW, int rows)
+{
+    LossPlan L;
+    return loss_plan(L, M, D, V, true, with_dW != 0, rows) ? L.bytes : 0;
+}
+
+extern "C" lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t *W, const int64_t *labels, int M, int D,
+                                              int V, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                              void *stream)
+{
+    set_launch_count(0);
+    LossPlan L;
+    if (M < 0 || D < 1 || V < 1) return LB_ERR_INVALID_ARG;
+    if (D % 8 || !loss_plan(L, M, D, V, false, false, 0)) return LB_ERR_UNSUPPORTED;
+    if (M == 0) return LB_OK;
+    if (!H || !W || !labels || !loss || !lse || !workspace) return LB_ERR_INVALID_ARG;
+    if (misaligned(H, 16) || misaligned(W, 16) || misaligned(labels, 8) || misaligned(loss, 4) || misaligned(lse, 4) ||
+        misaligned(workspace, 256) || workspace_bytes < L.bytes)
+        return LB_ERR_INVALID_ARG;
+    if ((size_t)((M + kMmTile - 1) / kMmTile) * L.ntn > (1u << 30)) return LB_ERR_UNSUPPORTED;
+    if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
+    unsigned char *ws = (unsigned char *)workspace;
+    cudaStream_t s = (cudaStream_t)stream;
+    const lb_status st = logits(L, H, W, labels, M, D, V, ws, false, s);
+    if (st != LB_OK) return st;
+    lse_kernel<<<(M + 7) / 8, 256, 0, s>>>((const float2 *)(ws + L.stat), (const float *)(ws + L.target), labels, M, V,
+                                           L.ntn, loss, lse);
+    set_launch_count(2);
+    return status_from(cudaGetLastError());
+}
+
+extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W, const int64_t *labels,
+                                               const float *weight, int M, int D, int V, int rows, float *loss,
+                                               uint16_t *dH, uint16_t *dW, void *workspace, size_t workspace_bytes,
+                                               void *stream)
+{
+    set_launch_count(0);
+    LossPlan L;
+    if (M < 0 || D < 1 || V < 1 || rows < 0) return LB_ERR_INVALID_ARG;
+    if (D % 8 || !loss_plan(L, M, D, V, true, dW != nullptr, rows)) return LB_ERR_UNSUPPORTED;
+    if (misaligned(dW, 16)) return LB_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (M == 0) {   // no rows: the gradient of W is zero
+        if (!dW) return LB_OK;
+        return status_from(cudaMemsetAsync(dW, 0, (size_t)V * D * 2, s));
+    }
+    if (!H || !W || !labels || !weight || !loss || !dH || !workspace) return LB_ERR_INVALID_ARG;
+    if (misaligned(H, 16) || misaligned(W, 16) || misaligned(labels, 8) || misaligned(weight, 4) ||
+        misaligned(loss, 4) || misaligned(dH, 16) || misaligned(workspace, 256) || workspace_bytes < L.bytes)
+        return LB_ERR_INVALID_ARG;
+    const size_t tiles_n = L.ntn, tiles_d = (D + kMmTile - 1) / kMmTile, tiles_m = (L.rows + kMmTile - 1) / kMmTile;
+    if (tiles_m * tiles_n > (1u << 28) || tiles_n * tiles_d > (1u << 28) || tiles_m * tiles_d * L.splits > (1u << 28))
+        return LB_ERR_UNSUPPORTED;
+    if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
+    unsigned char *ws = (unsigned char *)workspace;
+    int launches = 0;
+    for (int p = 0; p < L.npieces; ++p) {
+        const int r0 = p * L.rows, m = std::min(L.rows, M - r0);
+        const uint16_t *Hp = H + (size_t)r0 * D;
+        lb_status st = logits(L, Hp, W, labels + r0, m, D, V, ws, true, s);
+        if (st != LB_OK) return st;
+        const dim3 grid((L.Vp + kGradCols - 1) / kGradCols, m);
+        grad_kernel<<<grid, 256, 0, s>>>((uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
+                                         (const float *)(ws + L.target), labels + r0, weight + r0, V, L.Vp, L.ntn, D,
+                                         (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0);
+        launches += 2;
+        st = products(L, W, m, D, V, dH + (size_t)r0 * D, dW, p == 0, ws, s, &launches);
+        if (st != LB_OK) return st;
+    }
+    if (dW && L.npieces > 1) {
+        const size_t nvec = (size_t)V * D / 8;
+        const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
+        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.acc), 0, 1, nvec, (uint4 *)dW);
+        ++launches;
+    }
+    set_launch_count(launches);
+    return status_from(cudaGetLastError());
+}
+
+extern "C" lb_status lb_train_status(void *stream) { return loss_status((cudaStream_t)stream); }

@@ -1,0 +1,439 @@
+// Matrix products on pairs of SMs: the main loop shared by the training
+// operators (loss over the vocabulary, orthogonalised update).
+//
+//     D[i][j] = sum_k A(i, k) B(j, k),   16-bit operands, fp32 accumulation in tensor memory
+//
+// Either operand may be K-major (rows of k, as stored [i][k]) or MN-major
+// (stored [k][i]): the tensor core reads both, so no operand is transposed in
+// memory.  One output tile is 256 x 256 and belongs to a CTA pair
+// (tcgen05.mma.cta_group::2, M = 256): each CTA of the pair holds 128 of the
+// tile's i in its tensor memory and stages 128 i of A and 128 j of B per 64 k,
+// 32 KB for 128 x 256 x 64 multiply-adds.  A CTA by itself with the same
+// accumulator would have to stage 48 KB for them, and the operand stream from
+// L2 is what paces such a kernel.
+//
+// Roles (6 warps a CTA): warp 0 one thread issues the TMA copies of its CTA's
+// halves; warp 1 of the pair's first CTA one thread issues the MMAs for both;
+// warps 2-5 the epilogue (128 rows of the CTA, one thread a row).  Two
+// accumulators of 256 columns let the epilogue of one unit overlap the main
+// loop of the next.  Units (tile, or a k range of a tile) are dealt to the
+// pairs in order; a launch may hold several problems.
+//
+// A problem may contract several k segments that reuse its operands at an
+// offset in the slow coordinate ("parts"): hi * hi + hi * lo + lo * hi of
+// operands split into two halves runs as one main loop.
+//
+// Every wait is bounded: on timeout an error code is left in g_mm_err and
+// the kernel drains its copies and returns.
+#pragma once
+
+#include "lb_internal.cuh"
+#include "lb_tc.cuh"
+
+namespace lb {
+
+constexpr int kMmTile = 256;      // i and j of a unit
+constexpr int kMmHalf = 128;      // i and j one CTA of the pair stages
+constexpr int kMmBK = 64;         // k of a stage
+constexpr int kMmStages = 6;
+constexpr int kMmThreads = 192;
+constexpr uint32_t kMmOperand = kMmHalf * kMmBK * 2;   // 16 KB: one operand's half of one stage
+constexpr uint32_t kMmSlice = kMmBK * 128;             // MN-major: 64 k rows of 64 elements
+
+// Error code of a bounded wait that gave up, one per source file that has such kernels (mm_status).
+static __device__ int g_mm_err;
+
+struct MmSmem {
+    alignas(1024) unsigned char A[kMmStages][kMmOperand];
+    alignas(1024) unsigned char B[kMmStages][kMmOperand];
+    alignas(1024) unsigned char ST[4][32 * 128];   // one 32-row staging block per epilogue warp
+    uint64_t full[kMmStages], empty[kMmStages];
+    uint64_t accf[2], acce[2];
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr size_t kMmSmemBytes = sizeof(MmSmem) + 1024;
+
+// One problem of a launch.  a_mn / b_mn: the operand is MN-major.  part > 0: three k segments, in which the operand's
+// slow coordinate (the row of its array) is moved by lo_a / lo_b for the low halves.
+struct MmProb {
+    CUtensorMap mA, mB;
+    int a_mn, b_mn;
+    int parts, lo_a, lo_b;
+    int M, N;             // rows i, columns j
+    int nkb;              // 64-deep k blocks of one segment
+    int ntm, ntn;         // tiles
+    int m_fast;           // units run over i first (else over j first)
+    int splits, kb_per;   // k blocks are cut into `splits` ranges of kb_per
+    int unit0;            // first unit of this problem
+};
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+
+// shared::cluster address of this shared-memory object in CTA `rank` of the pair
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
+
+// Copy into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar_cluster)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];\n" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+
+// fp32 add of the block into global memory
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap *map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// fp32 accumulator, A and B both bf16 or both fp16, M = 256, N = 256
+__device__ __forceinline__ uint32_t mm_idesc(bool bf16, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(kMmTile >> 3) << 17) | ((uint32_t)(kMmTile >> 4) << 24);
+}
+
+struct MmUnit {
+    int q;             // problem
+    int tm, tn, split;
+    int kb0, kb1;      // k blocks [kb0, kb1) of the concatenated segments
+};
+
+template <int kMaxProbs>
+struct MmBatch {
+    MmProb p[kMaxProbs];
+    int n, nunits;
+    int extra;            // see mm_nth
+};
+
+// The k-th unit of a pair, -1 after its last.  Units are dealt in order, except that where a first problem of long units
+// leaves some pairs one short, those pairs first take `extra` units each of what follows, which fills the gap.
+template <int kMaxProbs>
+__device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, int pair, int npairs, int k)
+{
+    if (G.extra == 0) {
+        const int u = pair + k * npairs;
+        return u < G.nunits ? u : -1;
+    }
+    const int n0 = G.p[1].unit0, more = n0 % npairs;   // pairs below `more` have one long unit more
+    const int c0 = n0 / npairs + (pair < more ? 1 : 0);
+    if (k < c0) return pair + k * npairs;
+    k -= c0;
+    const int early = npairs - more;
+    if (pair >= more) {
+        if (k < G.extra) return n0 + (pair - more) + k * early;
+        k -= G.extra;
+    }
+    const int u = n0 + G.extra * early + pair + k * npairs;
+    return u < G.nunits ? u : -1;
+}
+
+template <int kMaxProbs>
+__device__ __forceinline__ MmUnit mm_unit(const MmBatch<kMaxProbs> &G, int u)
+{
+    MmUnit r;
+    r.q = 0;
+    for (int i = 1; i < G.n; ++i)
+        if (u >= G.p[i].unit0) r.q = i;
+    const MmProb &P = G.p[r.q];
+    int local = u - P.unit0;
+    const int tiles = P.ntm * P.ntn;
+    r.split = P.splits > 1 ? local / tiles : 0;
+    local -= r.split * tiles;
+    if (P.m_fast) {
+        r.tn = local / P.ntm;
+        r.tm = local - r.tn * P.ntm;
+    } else {
+        r.tm = local / P.ntn;
+        r.tn = local - r.tm * P.ntn;
+    }
+    const int total = P.nkb * P.parts;
+    r.kb0 = r.split * P.kb_per;
+    r.kb1 = min(total, r.kb0 + P.kb_per);
+    return r;
+}
+
+// What an epilogue gets for one unit: the accumulator columns `tmem` of this warp's 32 rows (row = row0 + lane).
+struct MmTileCtx {
+    uint32_t tmem;        // tensor-memory address: lane quarter in the upper half, first column in the lower
+    int row0;             // first of this warp's 32 rows
+    int col0;             // first of the 256 columns
+    int lane;
+    uint32_t st;          // this warp's 4 KB staging block (shared address)
+};
+
+// `Epi` has: struct Params; static __device__ void run(const Params &, const MmBatch &, const MmUnit &,
+// const MmTileCtx &, bool &stored); called by each epilogue warp once per unit.
+template <bool kBf16, int kMaxProbs, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+    mm_kernel(const __grid_constant__ MmBatch<kMaxProbs> G, const __grid_constant__ typename Epi::Params E)
+{
+    int *const err = &g_mm_err;
+    extern __shared__ __align__(1024) unsigned char mm_raw[];
+    const uint32_t raw_addr = smem_u32(mm_raw);
+    MmSmem &S = *reinterpret_cast<MmSmem *>(mm_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    volatile int *abort = &S.abort;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMmStages; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&S.accf[b], 1);
+            mbar_init(&S.acce[b], 8);   // four epilogue warps of each CTA (the first CTA's barrier is the one used)
+        }
+        S.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&S.tmem_base)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+
+    if (warp == 0) {
+        // ---------------- producer
+        if (lane == 0) {
+            uint32_t it = 0, pend = 0, pend_ph = 0;
+            for (int n = 0, u; (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                const MmUnit U = mm_unit(G, u);
+                const MmProb &P = G.p[U.q];
+                const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * kMmTile + (int)rank * kMmHalf;
+                for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
+                    const int s = it % kMmStages;
+                    const uint32_t ph = (it / kMmStages) & 1;
+                    if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
+                    if (rank == 0) mbar_expect_tx(&S.full[s], 4 * kMmOperand);   // both CTAs' halves
+                    const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
+                    const int seg = kc / P.nkb, k = (kc - seg * P.nkb) * kMmBK;
+                    const int oa = seg == 2 ? P.lo_a : 0, ob = seg == 1 ? P.lo_b : 0;
+                    if (P.a_mn) {
+                        tma_load_2d_pair(S.A[s], &P.mA, i0, k + oa, bar);
+                        tma_load_2d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k + oa, bar);
+                    } else {
+                        tma_load_2d_pair(S.A[s], &P.mA, k, i0 + oa, bar);
+                    }
+                    if (P.b_mn) {
+                        tma_load_2d_pair(S.B[s], &P.mB, j0, k + ob, bar);
+                        tma_load_2d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k + ob, bar);
+                    } else {
+                        tma_load_2d_pair(S.B[s], &P.mB, k, j0 + ob, bar);
+                    }
+                    pend |= 1u << s;
+                    pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
+                }
+            }
+            if (*abort) {
+                // let the copies already issued land before the pair leaves (bounded): the first CTA sees them on its
+                // barriers; the second, whose copies count there, waits a fixed time
+                const long long t0 = clock64();
+                if (rank == 0) {
+                    for (int s = 0; s < kMmStages; ++s)
+                        while ((pend >> s & 1) && !mbar_try_wait(&S.full[s], (pend_ph >> s) & 1) &&
+                               clock64() - t0 < kWaitCycles / 20) {
+                        }
+                } else {
+                    while (clock64() - t0 < kWaitCycles / 1000) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (first CTA of the pair)
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0, tcount = 0;
+            for (int u; (u = mm_nth(G, pair, npairs, (int)tcount)) >= 0 && !*abort; ++tcount) {
+                const MmUnit U = mm_unit(G, u);
+                const MmProb &P = G.p[U.q];
+                const int ab = tcount & 1;
+                const uint32_t aph = (tcount >> 1) & 1;
+                if (!mbar_wait(&S.acce[ab], aph ^ 1, abort, err, 2)) break;
+                tc_fence_after();
+                const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
+                const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn);
+                const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
+                // 16 k: 32 bytes along a K-major row, or two 8-row groups (2048 bytes) of an MN-major slice
+                const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
+                bool ok = true;
+                for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
+                    const int s = it % kMmStages;
+                    const uint32_t ph = (it / kMmStages) & 1;
+                    if (!mbar_wait(&S.full[s], ph, abort, err, 3)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = a_mn ? smem_desc_mn_sw128(S.A[s], kMmSlice) : smem_desc_sw128(S.A[s]);
+                    const uint64_t db = b_mn ? smem_desc_mn_sw128(S.B[s], kMmSlice) : smem_desc_sw128(S.B[s]);
+#pragma unroll
+                    for (int kk = 0; kk < kMmBK / 16; ++kk)
+                        tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, (kc > U.kb0 || kk) ? 1u : 0u);
+                    tc_commit_pair(&S.empty[s]);
+                }
+                if (!ok) break;
+                tc_commit_pair(&S.accf[ab]);
+            }
+        }
+    } else {
+        // ---------------- epilogue (warps 2-5: tensor-memory lanes 32 (warp % 4) ..)
+        const int q4 = warp & 3;
+        uint32_t tcount = 0;
+        bool stored = false;
+        MmTileCtx T;
+        T.lane = lane;
+        T.st = smem_u32(S.ST[q4]);
+        for (int u; (u = mm_nth(G, pair, npairs, (int)tcount)) >= 0 && !*abort; ++tcount) {
+            const MmUnit U = mm_unit(G, u);
+            const int ab = tcount & 1;
+            const uint32_t aph = (tcount >> 1) & 1;
+            if (!mbar_wait(&S.accf[ab], aph, abort, err, 4)) break;
+            tc_fence_after();
+            T.tmem = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(ab * kMmTile);
+            T.row0 = U.tm * kMmTile + (int)rank * kMmHalf + q4 * 32;
+            T.col0 = U.tn * kMmTile;
+            Epi::run(E, G, U, T, stored);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acce[ab]), 0));
+        }
+        if (lane == 0) tma_store_wait_all();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // no CTA of the pair leaves while the other may still signal it or use its operands
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+    }
+}
+
+// Host: an operand stored as rows of `cols` elements with `pitch` elements between rows.  K-major: a row is an i (or j)
+// and the box is 64 k x 128 rows; MN-major: a row is a k and the box is 64 i x 64 k rows.
+inline bool mm_operand(CUtensorMap *map, bool bf16, bool mn_major, const void *base, long rows, long cols, long pitch)
+{
+    return tmap_encode_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols,
+                          rows, pitch * 2, 64, mn_major ? kMmBK : kMmHalf);
+}
+
+// Host: tiles and k ranges of a problem whose k blocks are cut into (at most) `splits` ranges.
+inline void mm_plan(MmProb &P, int M, int N, long K, int parts, bool m_fast, int unit0, int splits)
+{
+    P.M = M;
+    P.N = N;
+    P.parts = parts;
+    P.nkb = (int)((K + kMmBK - 1) / kMmBK);
+    P.ntm = (M + kMmTile - 1) / kMmTile;
+    P.ntn = (N + kMmTile - 1) / kMmTile;
+    P.m_fast = m_fast ? 1 : 0;
+    P.unit0 = unit0;
+    const int total = P.nkb * parts;
+    P.kb_per = (total + splits - 1) / splits;
+    P.splits = (total + P.kb_per - 1) / P.kb_per;
+}
+// Host: CTA pairs that run at once on the current device.
+inline cudaError_t mm_pairs(int *pairs)
+{
+    int sms = 0;
+    const cudaError_t e = sm_count_of_current(&sms);
+    *pairs = sms / 2 > 0 ? sms / 2 : 1;
+    return e;
+}
+inline int mm_units(const MmProb &P) { return P.ntm * P.ntn * P.splits; }
+
+template <bool kBf16, int kMaxProbs, class Epi>
+inline cudaError_t mm_launch(const MmBatch<kMaxProbs> &G, const typename Epi::Params &E, cudaStream_t s)
+{
+    if (G.nunits == 0) return cudaSuccess;
+    const void *fn = (const void *)mm_kernel<kBf16, kMaxProbs, Epi>;
+    cudaError_t e = ensure_dyn_smem(fn, kMmSmemBytes);
+    if (e != cudaSuccess) return e;
+    int pairs = 0;
+    if ((e = mm_pairs(&pairs)) != cudaSuccess) return e;
+    if (pairs > G.nunits) pairs = G.nunits;
+    mm_kernel<kBf16, kMaxProbs, Epi><<<2 * pairs, kMmThreads, kMmSmemBytes, s>>>(G, E);
+    return cudaGetLastError();
+}
+
+// Host: waits for `s`, returns and clears this file's error code.
+static inline lb_status mm_status(cudaStream_t s)
+{
+    int code = 0;
+    const int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&code, g_mm_err, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return status_from(e);
+    if (!code) return LB_OK;
+    e = cudaMemcpyToSymbolAsync(g_mm_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return e == cudaSuccess ? LB_ERR_TIMEOUT : status_from(e);
+}
+
+}  // namespace lb

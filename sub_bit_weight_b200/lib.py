@@ -493,3 +493,117 @@ def lb_gemm_at_b(A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor, err: tor
                              _dev(D, torch.float32, "D"), Nc, Kc, Mr, Nc, _dev(alpha, torch.float32, "alpha"),
                              _dev(err, torch.int32, "err"), _stream(stream)), "lb_gemm_at_b")
     return D
+
+
+# ---------------------------------------------------------------------------
+# Operators of a training step around the layers (include/littlebit_train.h)
+# ---------------------------------------------------------------------------
+
+LB_F32, LB_BF16 = range(2)
+_DTYPE = {torch.float32: LB_F32, torch.bfloat16: LB_BF16}
+
+_sig("lb_cross_entropy_forward_workspace_bytes", ctypes.c_size_t, [_i, _i, _i])
+_sig("lb_cross_entropy_forward", _st, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("lb_cross_entropy_gradient_workspace_bytes", ctypes.c_size_t, [_i, _i, _i, _i, _i])
+_sig("lb_cross_entropy_gradient", _st, [_vp, _vp, _vp, _vp] + [_i] * 4 + [_vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("lb_train_status", _st, [_vp])
+
+
+class _On:
+    """The device of a call's tensors and its stream made current, so that what the call allocates belongs there."""
+
+    def __init__(self, stream, **tensors):
+        dev = None
+        for name, t in tensors.items():
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        self.device = dev
+        self._guard = None
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            self._guard = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(dev)
+        self._stream = stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        self.stream = (self._stream or torch.cuda.current_stream()).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _workspace(workspace, need: int, on: _On) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=on.device)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
+    return workspace
+
+
+def lb_train_status(stream=None) -> int:
+    """Synchronise and return (and clear) the status of the training operators' tensor-core kernels on the current
+    device: LB_OK or LB_ERR_TIMEOUT."""
+    return int(_lib.lb_train_status(_stream(stream)))
+
+
+def lb_cross_entropy_forward_workspace_bytes(M: int, D: int, V: int) -> int:
+    return int(_lib.lb_cross_entropy_forward_workspace_bytes(M, D, V))
+
+
+def lb_cross_entropy_gradient_workspace_bytes(M: int, D: int, V: int, head: bool = True, rows: int = 0) -> int:
+    return int(_lib.lb_cross_entropy_gradient_workspace_bytes(M, D, V, int(head), rows))
+
+
+def _loss_shapes(H, W, labels):
+    if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
+        raise ValueError("H must be [M, D] and W [V, D]")
+    _numel(labels, H.shape[0], "labels")
+    return H.shape[0], H.shape[1], W.shape[0]
+
+
+def lb_cross_entropy_forward(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """Softmax cross entropy of z = H W^T without keeping z: (loss [M], lse [M]) float32, for bfloat16 H [M, D] and
+    W [V, D] and int64 labels [M]; a label outside 0 .. V-1 (such as -100) gives loss 0."""
+    M, D, V = _loss_shapes(H, W, labels)
+    with _On(stream, H=H, W=W, labels=labels) as on:
+        loss, lse = (torch.empty(M, dtype=torch.float32, device=on.device) for _ in range(2))
+        ws = _workspace(workspace, lb_cross_entropy_forward_workspace_bytes(M, D, V), on)
+        _check(_lib.lb_cross_entropy_forward(_dev(H, torch.bfloat16, "H"), _dev(W, torch.bfloat16, "W"),
+                                             _dev(labels, torch.int64, "labels"), M, D, V, loss.data_ptr(),
+                                             lse.data_ptr(), _dev(ws, torch.uint8, "workspace"), ws.numel(),
+                                             on.stream), "lb_cross_entropy_forward")
+    return loss, lse
+
+
+def lb_cross_entropy_gradient(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weight: torch.Tensor,
+                              head: bool = True, rows: int = 0, workspace: torch.Tensor | None = None, stream=None):
+    """The loss with its gradients for float32 row weights [M] (d objective / d loss_m, 1 / count for a mean):
+    (loss [M] float32, dH [M, D] bfloat16, dW [V, D] bfloat16, or None with head=False: a frozen vocabulary matrix).
+    ``rows``: rows taken at a time (0: 8192), which bounds the workspace."""
+    M, D, V = _loss_shapes(H, W, labels)
+    _numel(weight, M, "weight")
+    with _On(stream, H=H, W=W, labels=labels, weight=weight) as on:
+        loss = torch.empty(M, dtype=torch.float32, device=on.device)
+        dH = torch.empty((M, D), dtype=torch.bfloat16, device=on.device)
+        dW = torch.empty((V, D), dtype=torch.bfloat16, device=on.device) if head else None
+        ws = _workspace(workspace, lb_cross_entropy_gradient_workspace_bytes(M, D, V, head, rows), on)
+        _check(_lib.lb_cross_entropy_gradient(_dev(H, torch.bfloat16, "H"), _dev(W, torch.bfloat16, "W"),
+                                              _dev(labels, torch.int64, "labels"),
+                                              _dev(weight, torch.float32, "weight"), M, D, V, rows, loss.data_ptr(),
+                                              dH.data_ptr(), dW.data_ptr() if head else None,
+                                              _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream),
+               "lb_cross_entropy_gradient")
+    return loss, dH, dW
