@@ -38,6 +38,31 @@ typedef enum lb_dtype {
 } lb_dtype;
 
 /*
+ * Token embedding: out[m] = scale * table[id_m], rounded once to the output type.
+ *   ids    int64 [M]; an id outside 0 .. V-1 (such as a padding -1) gives a row of zeros
+ *   table  table_dtype [V][D]        out  out_dtype [M][D]      (lb_dtype values)
+ * Arrays need the alignment of their elements (16 bytes and D a multiple of 8
+ * are fastest).  V, D >= 1; M = 0 is a valid empty call.
+ * Errors: LB_ERR_INVALID_ARG, LB_ERR_UNSUPPORTED (M >= 2^31, D > 2^25), LB_ERR_CUDA.
+ */
+LB_API lb_status lb_embedding_forward(const int64_t *ids, int64_t M, const void *table, int table_dtype, int V, int D,
+                                      float scale, void *out, int out_dtype, void *stream);
+
+/*
+ * Its gradient: dtable[v] = scale * (sum of dout[m] over the m with id_m = v),
+ * zeros for a row that no id names; the whole of dtable is overwritten.  The
+ * sums are float32, by increasing m within groups of the sorted tokens (a
+ * fixed order: the same bits every time), times scale, rounded once.
+ *   dout  dout_dtype [M][D]          dtable  dtable_dtype [V][D]
+ * An id outside 0 .. V-1 adds nothing.  M = 0 writes zeros.
+ * Errors: LB_ERR_INVALID_ARG, LB_ERR_UNSUPPORTED (M >= 2^31, D > 2^23), LB_ERR_CUDA.
+ */
+LB_API size_t lb_embedding_backward_workspace_bytes(int64_t M, int V, int D);
+LB_API lb_status lb_embedding_backward(const int64_t *ids, int64_t M, const void *dout, int dout_dtype, int V, int D,
+                                       float scale, void *dtable, int dtable_dtype, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
  * Softmax cross entropy against a vocabulary matrix, without the logits:
  *     z = H W^T [M x V],  lse_m = log sum_v exp z_mv,  loss_m = lse_m - z_m,label(m)
  *

@@ -1,0 +1,428 @@
+// Token embedding: lookup with scaling, and its gradient by sorted tokens.
+//
+//     out[m] = scale * table[id_m]             dtable[v] = scale * sum over m with id_m = v of dout[m]
+//
+// Both are bound by memory.  The lookup reads the rows it names and writes M D
+// elements.  The gradient reads M D elements and writes all V D (rows without
+// a token are zero), in a fixed order of additions:
+//
+//   1  the blocks 0 .. C-1 each sort up to 16,384 (id, position) pairs in
+//      shared memory (bitonic; the pairs are distinct, so the order is unique)
+//      while the other blocks write the zeros of the rows that no token names,
+//      most of the output in a real vocabulary;
+//   2  (C > 1) every pair finds its place among the other blocks' sorted runs;
+//   3  a block takes 32 consecutive pairs and 256 vectors of columns, adds the
+//      rows of each token in float32 and writes the tokens that lie inside its
+//      32 pairs; a token that crosses into other blocks (a frequent one)
+//      leaves float32 partial sums there;
+//   4  the partial sums of each crossing token are added in order.
+
+#include <algorithm>
+#include <cstring>
+
+#include "lb_internal.cuh"
+#include "littlebit_train.h"
+
+namespace lb {
+namespace {
+
+constexpr int kSortMost = 16384;    // pairs one block sorts (128 KB of shared memory)
+constexpr int kSumPairs = 32;       // sorted pairs one block of step 3 adds
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+    T v[N];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x)
+{
+    return x;
+}
+template <>
+__device__ __forceinline__ uint16_t from_f<uint16_t>(float x)
+{
+    uint16_t r;
+    asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(r) : "f"(x));
+    return r;
+}
+
+// ---- lookup: one row per blockIdx.x, up to 4 vectors a thread in flight
+template <typename TI, typename TO, int N>
+__global__ void __launch_bounds__(256) lookup_kernel(const int64_t *__restrict__ ids, const TI *__restrict__ table,
+                                                     long long V, int D, float scale, TO *__restrict__ out)
+{
+    const long long id = ids[blockIdx.x];
+    const bool ok = id >= 0 && id < V;
+    const int nv = D / N;
+    const Vec<TI, N> *src = reinterpret_cast<const Vec<TI, N> *>(table + (ok ? id : 0) * (long long)D);
+    Vec<TO, N> *dst = reinterpret_cast<Vec<TO, N> *>(out + (long long)blockIdx.x * D);
+    const int c0 = blockIdx.y * 1024 + threadIdx.x;
+    Vec<TI, N> x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (ok && c0 + 256 * j < nv) x[j] = src[c0 + 256 * j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (c0 + 256 * j >= nv) break;
+        Vec<TO, N> y;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y.v[i] = ok ? from_f<TO>(to_f(x[j].v[i]) * scale) : from_f<TO>(0.0f);
+        dst[c0 + 256 * j] = y;
+    }
+}
+
+// ---- 1: sort, and zeros of the rows without a token
+// Pairs are (id << 32 | position); an id outside 0 .. V-1 sorts behind every other, as V.
+template <int N, typename TO>
+__global__ void __launch_bounds__(1024) sort_zero_kernel(const int64_t *__restrict__ ids, long long M, int V, int D,
+                                                         int nsort, int chunk, unsigned long long *__restrict__ pairs,
+                                                         TO *__restrict__ out)
+{
+    extern __shared__ __align__(16) unsigned char e_raw[];
+    if ((int)blockIdx.x < nsort) {
+        unsigned long long *k = reinterpret_cast<unsigned long long *>(e_raw);
+        const long long base = (long long)blockIdx.x * chunk;
+        const int n = (int)min((long long)chunk, M - base);
+        int p2 = 32;
+        while (p2 < n) p2 <<= 1;
+        for (int i = threadIdx.x; i < p2; i += 1024) {
+            unsigned long long key = ~0ull;
+            if (i < n) {
+                const long long id = ids[base + i];
+                key = ((unsigned long long)(id >= 0 && id < V ? (uint32_t)id : (uint32_t)V) << 32) | (uint32_t)(base + i);
+            }
+            k[i] = key;
+        }
+        for (int size = 2; size <= p2; size <<= 1)
+            for (int step = size >> 1; step > 0; step >>= 1) {
+                // steps below 32 stay inside one warp's 64 consecutive pairs
+                if (step >= 32 || step == size >> 1) __syncthreads();
+                else __syncwarp();
+                for (int i = threadIdx.x; i < p2 >> 1; i += 1024) {
+                    const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+                    const unsigned long long a = k[lo], b = k[hi];
+                    if ((a > b) == ((lo & size) == 0)) {
+                        k[lo] = b;
+                        k[hi] = a;
+                    }
+                }
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += 1024) pairs[base + i] = k[i];
+        return;
+    }
+    // rows [v0, v1) of the vocabulary belong to this block
+    const int nz = gridDim.x - nsort, b = blockIdx.x - nsort;
+    const int per = (V + nz - 1) / nz;
+    unsigned char *seen = e_raw;
+    for (long long v0 = (long long)b * per, end = min((long long)V, v0 + per); v0 < end; v0 += kSortMost) {
+        const int rows = (int)min((long long)kSortMost, end - v0);
+        for (int i = threadIdx.x; i < rows; i += 1024) seen[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (long long i = threadIdx.x; i < M; i += 1024) {
+            const long long r = ids[i] - v0;
+            if (r >= 0 && r < rows) seen[r] = 1;
+        }
+        __syncthreads();
+        Vec<TO, N> zero;
+#pragma unroll
+        for (int i = 0; i < N; ++i) zero.v[i] = 0;
+        const int nv = D / N;
+        for (int r = threadIdx.x >> 7; r < rows; r += 8) {   // 128 threads a row
+            if (seen[r]) continue;
+            Vec<TO, N> *dst = reinterpret_cast<Vec<TO, N> *>(out + (v0 + r) * (long long)D);
+            for (int i = threadIdx.x & 127; i < nv; i += 128) dst[i] = zero;
+        }
+        __syncthreads();
+    }
+}
+
+// ---- 2: place of every pair in the union of the sorted chunks
+__global__ void __launch_bounds__(256) merge_kernel(const unsigned long long *__restrict__ in, long long M, int nsort,
+                                                    int chunk, unsigned long long *__restrict__ out)
+{
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= M) return;
+    const unsigned long long key = in[i];
+    const int own = (int)(i / chunk);
+    long long at = i - (long long)own * chunk;
+    for (int c = 0; c < nsort; ++c) {
+        if (c == own) continue;
+        const unsigned long long *p = in + (long long)c * chunk;
+        int lo = 0, hi = (int)min((long long)chunk, M - (long long)c * chunk);
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p[mid] < key) lo = mid + 1;
+            else hi = mid;
+        }
+        at += lo;
+    }
+    out[at] = key;
+}
+
+// ---- 3: sums of 32 pairs.  A token whose pairs begin before or end after this block's leaves its sum in part[2 b]
+// (it began before; also a token that fills the block) or part[2 b + 1] (it begins here and goes on).
+template <typename TI, typename TO, int N>
+__global__ void __launch_bounds__(256) sum_kernel(const unsigned long long *__restrict__ pairs, long long M, int V, int D,
+                                                  const TI *__restrict__ dout, float scale, TO *__restrict__ out,
+                                                  float *__restrict__ part)
+{
+    __shared__ unsigned long long k[kSumPairs + 2];   // the pair before, 32 pairs, the pair after (~0 where there is none)
+    const long long base = (long long)blockIdx.x * kSumPairs;
+    const int n = (int)min((long long)kSumPairs, M - base);
+    if (threadIdx.x < kSumPairs + 2) {
+        const long long i = base + (int)threadIdx.x - 1;
+        k[threadIdx.x] = i >= 0 && i < M && (int)threadIdx.x <= n + 1 ? pairs[i] : ~0ull;
+    }
+    __syncthreads();
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c >= D / N) return;
+    float acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    int first = 0;   // first pair of the current token in this block
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+        Vec<TI, N> x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + u < n && (int)(k[i0 + u + 1] >> 32) < V)
+                x[u] = reinterpret_cast<const Vec<TI, N> *>(dout + (long long)(uint32_t)k[i0 + u + 1] * D)[c];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const uint32_t id = (uint32_t)(k[i + 1] >> 32);
+            if ((int)id >= V) return;   // the rest names no row
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += to_f(x[u].v[j]);
+            const bool last = i + 1 == n;
+            if (last || (uint32_t)(k[i + 2] >> 32) != id) {
+                const bool before = first == 0 && (uint32_t)(k[0] >> 32) == id;
+                const bool after = last && (uint32_t)(k[i + 2] >> 32) == id;
+                if (before || after) {
+                    Vec<float, N> *p = reinterpret_cast<Vec<float, N> *>(
+                        part + ((long long)blockIdx.x * 2 + (before ? 0 : 1)) * D);
+                    Vec<float, N> y;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) y.v[j] = acc[j];
+                    p[c] = y;
+                } else {
+                    Vec<TO, N> y;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) y.v[j] = from_f<TO>(acc[j] * scale);
+                    reinterpret_cast<Vec<TO, N> *>(out + (long long)id * D)[c] = y;
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                first = i + 1;
+            }
+        }
+    }
+}
+
+// ---- 4: a token that begins in block b's pairs and goes on past them
+template <typename TO, int N>
+__global__ void __launch_bounds__(256) join_kernel(const unsigned long long *__restrict__ pairs, long long M, int V, int D,
+                                                   const float *__restrict__ part, float scale, TO *__restrict__ out)
+{
+    const long long b = blockIdx.x, lastp = (b + 1) * kSumPairs - 1;
+    if (lastp + 1 >= M) return;
+    const uint32_t id = (uint32_t)(pairs[lastp] >> 32);
+    if ((int)id >= V || (uint32_t)(pairs[lastp + 1] >> 32) != id) return;   // nothing goes on
+    if (b > 0 && (uint32_t)(pairs[b * kSumPairs - 1] >> 32) == id) return;  // it began before this block
+    // last block that holds a pair of this token: pairs are sorted, so search for the first larger id
+    long long lo = lastp + 1, hi = M;
+    while (lo < hi) {
+        const long long mid = (lo + hi) >> 1;
+        if ((uint32_t)(pairs[mid] >> 32) <= id) lo = mid + 1;
+        else hi = mid;
+    }
+    const long long e = (lo - 1) / kSumPairs;
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c >= D / N) return;
+    Vec<float, N> a = reinterpret_cast<const Vec<float, N> *>(part + (2 * b + 1) * D)[c];
+#pragma unroll 4
+    for (long long q = b + 1; q <= e; ++q) {
+        const Vec<float, N> x = reinterpret_cast<const Vec<float, N> *>(part + 2 * q * D)[c];
+#pragma unroll
+        for (int j = 0; j < N; ++j) a.v[j] += x.v[j];
+    }
+    Vec<TO, N> y;
+#pragma unroll
+    for (int j = 0; j < N; ++j) y.v[j] = from_f<TO>(a.v[j] * scale);
+    reinterpret_cast<Vec<TO, N> *>(out + (long long)id * D)[c] = y;
+}
+
+// ---- host
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+size_t size_of(int dt) { return dt == LB_F32 ? 4 : 2; }
+bool known(int dt) { return dt == LB_F32 || dt == LB_BF16; }
+bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+// Largest vector (in elements, at most `most`) that divides a row and to which both arrays are aligned.
+int vector_of(int D, int most, const void *a, size_t sa, const void *b, size_t sb)
+{
+    int n = most;
+    while (n > 1 && (D % n || misaligned(a, n * sa) || misaligned(b, n * sb))) n >>= 1;
+    return n;
+}
+
+struct EmbedPlan {
+    int nsort, chunk;
+    long long nsum;
+    size_t pairs, sorted, part, bytes;
+};
+
+bool embed_plan(EmbedPlan &L, long long M, int V, int D)
+{
+    if (M < 0 || V < 1 || D < 1 || M > (1LL << 31) - 1) return false;
+    // equal chunks: the largest block's sort is what the others wait for
+    const long long c = M ? (M + kSortMost - 1) / kSortMost : 0;
+    L.nsort = (int)c;
+    L.chunk = c ? (int)((M + c - 1) / c) : 0;
+    L.nsum = (M + kSumPairs - 1) / kSumPairs;
+    size_t at = 0;
+    auto take = [&](size_t b) {
+        const size_t o = at;
+        at = up256(at + b);
+        return o;
+    };
+    L.pairs = take((size_t)M * 8);
+    L.sorted = take(c > 1 ? (size_t)M * 8 : 0);
+    L.part = take((size_t)L.nsum * 2 * D * 4);
+    L.bytes = at;
+    return true;
+}
+
+template <typename TI, typename TO, int N>
+cudaError_t launch_lookup(const int64_t *ids, long long M, const void *table, int V, int D, float scale, void *out,
+                          cudaStream_t s)
+{
+    const dim3 grid((unsigned)M, (D / N + 1023) / 1024);
+    lookup_kernel<TI, TO, N><<<grid, 256, 0, s>>>(ids, (const TI *)table, V, D, scale, (TO *)out);
+    return cudaGetLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t lookup(int n, const int64_t *ids, long long M, const void *table, int V, int D, float scale, void *out,
+                   cudaStream_t s)
+{
+    constexpr int kMost = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+    if constexpr (kMost == 8)
+        if (n == 8) return launch_lookup<TI, TO, 8>(ids, M, table, V, D, scale, out, s);
+    if (n == 4) return launch_lookup<TI, TO, 4>(ids, M, table, V, D, scale, out, s);
+    if (n == 2) return launch_lookup<TI, TO, 2>(ids, M, table, V, D, scale, out, s);
+    return launch_lookup<TI, TO, 1>(ids, M, table, V, D, scale, out, s);
+}
+
+template <typename TI, typename TO, int N>
+cudaError_t launch_grad(const EmbedPlan &L, const int64_t *ids, long long M, const void *dout, int V, int D, float scale,
+                        void *dtable, unsigned char *ws, cudaStream_t s, int *launches)
+{
+    int sms = 0;
+    cudaError_t e = sm_count_of_current(&sms);
+    if (e != cudaSuccess) return e;
+    // shared memory: the chunk's pairs, rounded up to a power of two, or the flags of a block's rows
+    size_t p2 = 32;
+    while (p2 < (size_t)L.chunk) p2 <<= 1;
+    const int nz = (int)std::min<long long>(V, std::max(sms - L.nsort, 32));
+    const size_t flags = std::min<size_t>((V + nz - 1) / nz, kSortMost);
+    const size_t smem = std::max(L.nsort ? p2 * 8 : 0, flags);
+    const void *fn = (const void *)sort_zero_kernel<N, TO>;
+    if ((e = ensure_dyn_smem(fn, smem)) != cudaSuccess) return e;
+    unsigned long long *pairs = (unsigned long long *)(ws + L.pairs);
+    sort_zero_kernel<N, TO><<<L.nsort + nz, 1024, smem, s>>>(ids, M, V, D, L.nsort, L.chunk, pairs, (TO *)dtable);
+    ++*launches;
+    if (M > 0) {
+        if (L.nsort > 1) {
+            unsigned long long *sorted = (unsigned long long *)(ws + L.sorted);
+            merge_kernel<<<(unsigned)((M + 255) / 256), 256, 0, s>>>(pairs, M, L.nsort, L.chunk, sorted);
+            pairs = sorted;
+            ++*launches;
+        }
+        float *part = (float *)(ws + L.part);
+        const dim3 grid((unsigned)L.nsum, (D / N + 255) / 256);
+        sum_kernel<TI, TO, N><<<grid, 256, 0, s>>>(pairs, M, V, D, (const TI *)dout, scale, (TO *)dtable, part);
+        join_kernel<TO, N><<<grid, 256, 0, s>>>(pairs, M, V, D, part, scale, (TO *)dtable);
+        *launches += 2;
+    }
+    return cudaGetLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t grad(int n, const EmbedPlan &L, const int64_t *ids, long long M, const void *dout, int V, int D, float scale,
+                 void *dtable, unsigned char *ws, cudaStream_t s, int *launches)
+{
+    if (n == 4) return launch_grad<TI, TO, 4>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
+    if (n == 2) return launch_grad<TI, TO, 2>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
+    return launch_grad<TI, TO, 1>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
+}
+
+}  // namespace
+}  // namespace lb
+
+using namespace lb;
+
+extern "C" lb_status lb_embedding_forward(const int64_t *ids, int64_t M, const void *table, int table_dtype, int V, int D,
+                                          float scale, void *out, int out_dtype, void *stream)
+{
+    set_launch_count(0);
+    if (M < 0 || V < 1 || D < 1 || !known(table_dtype) || !known(out_dtype)) return LB_ERR_INVALID_ARG;
+    if (M > (1LL << 31) - 1 || D > (1 << 25)) return LB_ERR_UNSUPPORTED;
+    if (M == 0) return LB_OK;
+    const size_t si = size_of(table_dtype), so = size_of(out_dtype);
+    if (!ids || !table || !out || misaligned(ids, 8) || misaligned(table, si) || misaligned(out, so))
+        return LB_ERR_INVALID_ARG;
+    const int n = vector_of(D, si == 2 && so == 2 ? 8 : 4, table, si, out, so);
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (table_dtype == LB_F32)
+        e = out_dtype == LB_F32 ? lookup<float, float>(n, ids, M, table, V, D, scale, out, s)
+                                : lookup<float, uint16_t>(n, ids, M, table, V, D, scale, out, s);
+    else
+        e = out_dtype == LB_F32 ? lookup<uint16_t, float>(n, ids, M, table, V, D, scale, out, s)
+                                : lookup<uint16_t, uint16_t>(n, ids, M, table, V, D, scale, out, s);
+    set_launch_count(1);
+    return status_from(e);
+}
+
+extern "C" size_t lb_embedding_backward_workspace_bytes(int64_t M, int V, int D)
+{
+    EmbedPlan L;
+    return embed_plan(L, M, V, D) ? L.bytes : 0;
+}
+
+extern "C" lb_status lb_embedding_backward(const int64_t *ids, int64_t M, const void *dout, int dout_dtype, int V, int D,
+                                           float scale, void *dtable, int dtable_dtype, void *workspace,
+                                           size_t workspace_bytes, void *stream)
+{
+    set_launch_count(0);
+    EmbedPlan L;
+    if (M < 0 || V < 1 || D < 1 || !known(dout_dtype) || !known(dtable_dtype)) return LB_ERR_INVALID_ARG;
+    if (D > (1 << 23) || !embed_plan(L, M, V, D)) return LB_ERR_UNSUPPORTED;
+    const size_t si = size_of(dout_dtype), so = size_of(dtable_dtype);
+    if (!dtable || misaligned(dtable, so)) return LB_ERR_INVALID_ARG;
+    if (M > 0 && (!ids || !dout || !workspace || misaligned(ids, 8) || misaligned(dout, si) ||
+                  misaligned(workspace, 256) || workspace_bytes < L.bytes))
+        return LB_ERR_INVALID_ARG;
+    const int n = vector_of(D, 4, M ? dout : dtable, M ? si : so, dtable, so);
+    unsigned char *ws = (unsigned char *)workspace;
+    cudaStream_t s = (cudaStream_t)stream;
+    int launches = 0;
+    cudaError_t e;
+    if (dout_dtype == LB_F32)
+        e = dtable_dtype == LB_F32 ? grad<float, float>(n, L, ids, M, dout, V, D, scale, dtable, ws, s, &launches)
+                                   : grad<float, uint16_t>(n, L, ids, M, dout, V, D, scale, dtable, ws, s, &launches);
+    else
+        e = dtable_dtype == LB_F32 ? grad<uint16_t, float>(n, L, ids, M, dout, V, D, scale, dtable, ws, s, &launches)
+                                   : grad<uint16_t, uint16_t>(n, L, ids, M, dout, V, D, scale, dtable, ws, s, &launches);
+    set_launch_count(launches);
+    return status_from(e);
+}

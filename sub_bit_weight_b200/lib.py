@@ -502,6 +502,9 @@ def lb_gemm_at_b(A: torch.Tensor, B: torch.Tensor, alpha: torch.Tensor, err: tor
 LB_F32, LB_BF16 = range(2)
 _DTYPE = {torch.float32: LB_F32, torch.bfloat16: LB_BF16}
 
+_sig("lb_embedding_forward", _st, [_vp, _i64, _vp, _i, _i, _i, ctypes.c_float, _vp, _i, _vp])
+_sig("lb_embedding_backward_workspace_bytes", ctypes.c_size_t, [_i64, _i, _i])
+_sig("lb_embedding_backward", _st, [_vp, _i64, _vp, _i, _i, _i, ctypes.c_float, _vp, _i, _vp, ctypes.c_size_t, _vp])
 _sig("lb_cross_entropy_forward_workspace_bytes", ctypes.c_size_t, [_i, _i, _i])
 _sig("lb_cross_entropy_forward", _st, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("lb_cross_entropy_gradient_workspace_bytes", ctypes.c_size_t, [_i, _i, _i, _i, _i])
@@ -556,6 +559,51 @@ def lb_train_status(stream=None) -> int:
     """Synchronise and return (and clear) the status of the training operators' tensor-core kernels on the current
     device: LB_OK or LB_ERR_TIMEOUT."""
     return int(_lib.lb_train_status(_stream(stream)))
+
+
+def _element(dtype, name: str) -> int:
+    if dtype not in _DTYPE:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _DTYPE[dtype]
+
+
+def lb_embedding_forward(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0, dtype: torch.dtype | None = None,
+                         stream=None) -> torch.Tensor:
+    """scale * table[ids]: int64 ids of any shape, table [V, D] float32 or bfloat16 -> [*ids.shape, D] of ``dtype``
+    (default: the table's).  An id outside 0 .. V-1 (such as a padding -1) gives zeros."""
+    if table.dim() != 2:
+        raise ValueError("table must be [V, D]")
+    V, D = table.shape
+    dtype = table.dtype if dtype is None else dtype
+    with _On(stream, ids=ids, table=table) as on:
+        out = torch.empty((*ids.shape, D), dtype=dtype, device=on.device)
+        _check(_lib.lb_embedding_forward(_dev(ids, torch.int64, "ids"), ids.numel(),
+                                         _dev(table, table.dtype, "table"), _element(table.dtype, "table"), V, D,
+                                         float(scale), out.data_ptr(), _element(dtype, "dtype"), on.stream),
+               "lb_embedding_forward")
+    return out
+
+
+def lb_embedding_backward_workspace_bytes(M: int, V: int, D: int) -> int:
+    return int(_lib.lb_embedding_backward_workspace_bytes(M, V, D))
+
+
+def lb_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, scale: float = 1.0,
+                          dtype: torch.dtype = torch.float32, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Gradient [V, D] (``dtype``) of lb_embedding_forward by the table, for dout [*ids.shape, D] float32 or bfloat16:
+    sums in float32 in a fixed order, zeros for rows without a token."""
+    if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout must be [*ids.shape, D]")
+    M, D = ids.numel(), dout.shape[-1]
+    with _On(stream, ids=ids, dout=dout) as on:
+        dtable = torch.empty((V, D), dtype=dtype, device=on.device)
+        ws = _workspace(workspace, lb_embedding_backward_workspace_bytes(M, V, D), on)
+        _check(_lib.lb_embedding_backward(_dev(ids, torch.int64, "ids"), M, _dev(dout, dout.dtype, "dout"),
+                                          _element(dout.dtype, "dout"), V, D, float(scale), dtable.data_ptr(),
+                                          _element(dtype, "dtype"), _dev(ws, torch.uint8, "workspace"), ws.numel(),
+                                          on.stream), "lb_embedding_backward")
+    return dtable
 
 
 def lb_cross_entropy_forward_workspace_bytes(M: int, D: int, V: int) -> int:
