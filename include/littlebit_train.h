@@ -103,6 +103,31 @@ LB_API lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W,
                                            uint16_t *dH, uint16_t *dW, void *workspace, size_t workspace_bytes,
                                            void *stream);
 
+/*
+ * Orthogonalised updates, for the gradients of latent factors (dU, dV of
+ * lb_layer_backward, or their running mean): for each matrix, by the
+ * Newton-Schulz iteration of the Muon optimiser,
+ *     X = G / (|G|_F + eps);   `steps` times:  
+ *     X <- a X + b (X X^T) X + c (X X^T)^2 X,   (a, b, c) = (3.4445, -4.7750, 2.0315)
+ * which carries every singular value that is not tiny close to 1.
+ *
+ *   G      [n] pointers to dtype [rows_i][cols_i] (lb_dtype), aligned to their elements
+ *   rows, cols   HOST int [n], >= 1; min(rows, cols) <= LB_MAX_RANK
+ *   steps  1 .. 10 (5 is usual);  eps >= 0 (1e-7 is usual)
+ *   O      [n] pointers to bfloat16 [rows_i][cols_i], overwritten
+ * n = 0 is a valid empty call; all matrices of a call share its launches, so
+ * pass a block's latents together.  Float32 in effect: products take operands
+ * of 22 bits and accumulate in float32, the result is rounded once.  A matrix
+ * of zeros gives zeros; one with a NaN or an infinity gives NaN throughout,
+ * and touches no other matrix.
+ * Errors: LB_ERR_INVALID_ARG, LB_ERR_UNSUPPORTED (steps > 10, min(rows, cols)
+ * > LB_MAX_RANK, a side above 2^24), LB_ERR_OOM (host memory), LB_ERR_CUDA.
+ */
+LB_API size_t lb_orthogonalise_workspace_bytes(const int *rows, const int *cols, int n, int dtype);
+LB_API lb_status lb_orthogonalise(const void *const *G, int dtype, const int *rows, const int *cols, int n, int steps,
+                                  float eps, uint16_t *const *O, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
 /* Device-side status of the tensor-core kernels of this header on the current
  * device: synchronises `stream`, returns LB_ERR_TIMEOUT if a bounded wait gave
  * up since the last check (the outputs of that call are unspecified) and

@@ -377,7 +377,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     MmBatch<1> G;
     memset(&G, 0, sizeof(G));
     G.n = 1;
-    mm_plan(G.p[0], M, V, D, 1, true, 0, 1);
+    mm_plan(G.p[0], M, V, D, true, 0, 1);
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.p[0].mA, true, false, H, M, D, D) || !mm_operand(&G.p[0].mB, true, false, W, V, D, D))
         return LB_ERR_INVALID_ARG;
@@ -412,7 +412,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     memset(&E, 0, sizeof(E));
     const void *Gm = ws + L.E;
     MmProb &P = G.p[0];
-    mm_plan(P, M, D, V, 1, true, 0, L.splits);
+    mm_plan(P, M, D, V, true, 0, L.splits);
     P.b_mn = 1;
     if (!mm_operand(&P.mA, true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&P.mB, true, true, W, V, D, D))
         return LB_ERR_INVALID_ARG;
@@ -432,7 +432,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     G.nunits = mm_units(P);
     if (dW) {
         MmProb &Q = G.p[1];
-        mm_plan(Q, V, D, M, 1, false, G.nunits, 1);
+        mm_plan(Q, V, D, M, false, G.nunits, 1);
         Q.a_mn = Q.b_mn = 1;
         if (!mm_operand(&Q.mA, true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&Q.mB, true, true, ws + L.Hc, M, D, D))
             return LB_ERR_INVALID_ARG;
@@ -468,7 +468,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
 
 }  // namespace
 
-lb_status loss_status(cudaStream_t s) { return mm_status(s); }
+lb_status orth_status(cudaStream_t s);
 
 }  // namespace lb
 
@@ -559,4 +559,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     return status_from(cudaGetLastError());
 }
 
-extern "C" lb_status lb_train_status(void *stream) { return loss_status((cudaStream_t)stream); }
+extern "C" lb_status lb_train_status(void *stream)
+{
+    const lb_status a = mm_status((cudaStream_t)stream), b = orth_status((cudaStream_t)stream);
+    return a != LB_OK ? a : b;
+}

@@ -19,9 +19,11 @@
 // loop of the next.  Units (tile, or a k range of a tile) are dealt to the
 // pairs in order; a launch may hold several problems.
 //
-// A problem may contract several k segments that reuse its operands at an
-// offset in the slow coordinate ("parts"): hi * hi + hi * lo + lo * hi of
-// operands split into two halves runs as one main loop.
+// A problem is a batch of equal products, its operands arrays [z][row][column].
+// With parts = 3 each operand is a pair of halves (the planes z and z + 1: high
+// and low), and hi * hi + hi * lo + lo * hi runs as one main loop three times as
+// long; with parts = 2 one operand is whole and only the other has a low half.
+// A problem marked symmetric has only its tiles on and above the diagonal.
 //
 // Every wait is bounded: on timeout an error code is left in g_mm_err and
 // the kernel drains its copies and returns.
@@ -54,17 +56,19 @@ struct MmSmem {
 };
 constexpr size_t kMmSmemBytes = sizeof(MmSmem) + 1024;
 
-// One problem of a launch.  a_mn / b_mn: the operand is MN-major.  part > 0: three k segments, in which the operand's
-// slow coordinate (the row of its array) is moved by lo_a / lo_b for the low halves.
+// One problem of a launch: `batch` products of M x N over nkb 64-deep k blocks, three times as many with parts = 3.
+// a_mn / b_mn: the operand is MN-major.  za, zb: its z planes from one product of the batch to the next.
 struct MmProb {
     CUtensorMap mA, mB;
     int a_mn, b_mn;
-    int parts, lo_a, lo_b;
+    int parts, za, zb;
+    int b_whole;          // with parts = 2: the low half taken is A's (else B's)
     int M, N;             // rows i, columns j
-    int nkb;              // 64-deep k blocks of one segment
-    int ntm, ntn;         // tiles
+    int nkb;
+    int ntm, ntn, tiles;  // tiles across, along, and in all (fewer than across times along when symmetric)
     int m_fast;           // units run over i first (else over j first)
-    int splits, kb_per;   // k blocks are cut into `splits` ranges of kb_per
+    int sym;
+    int batch, splits, kb_per;   // k blocks are cut into `splits` ranges of kb_per
     int unit0;            // first unit of this problem
 };
 
@@ -94,12 +98,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 }
 
 // Copy into this CTA's shared memory, counted on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar_cluster)
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                                 uint32_t bar_cluster)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];\n" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(bar_cluster)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], "
+        "[%1, {%2, %3, %4}], [%5];\n" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
         : "memory");
 }
 
@@ -107,6 +112,14 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int 
 {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x),
                  "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int x, int y, int z, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(src)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
 }
@@ -145,16 +158,18 @@ __device__ __forceinline__ void tc_mma_f16_pair(uint32_t tmem_d, uint64_t adesc,
         : "memory");
 }
 
-// fp32 accumulator, A and B both bf16 or both fp16, M = 256, N = 256
-__device__ __forceinline__ uint32_t mm_idesc(bool bf16, bool a_mn, bool b_mn)
+// fp32 accumulator, A and B both bf16 or both fp16, M = 256, N = n (a multiple of 32)
+__device__ __forceinline__ uint32_t mm_idesc(bool bf16, bool a_mn, bool b_mn, int n)
 {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(kMmTile >> 3) << 17) | ((uint32_t)(kMmTile >> 4) << 24);
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMmTile >> 4) << 24);
 }
 
 struct MmUnit {
     int q;             // problem
+    int b;             // product of its batch
     int tm, tn, split;
+    int half;          // columns one CTA stages: half the tile's, 128 except in the last column of tiles
     int kb0, kb1;      // k blocks [kb0, kb1) of the concatenated segments
 };
 
@@ -195,17 +210,25 @@ __device__ __forceinline__ MmUnit mm_unit(const MmBatch<kMaxProbs> &G, int u)
     for (int i = 1; i < G.n; ++i)
         if (u >= G.p[i].unit0) r.q = i;
     const MmProb &P = G.p[r.q];
+    // ranges of k outermost: the units in flight share operands
     int local = u - P.unit0;
-    const int tiles = P.ntm * P.ntn;
-    r.split = P.splits > 1 ? local / tiles : 0;
-    local -= r.split * tiles;
-    if (P.m_fast) {
+    const int per_range = P.tiles * P.batch;
+    r.split = P.splits > 1 ? local / per_range : 0;
+    local -= r.split * per_range;
+    r.b = P.batch > 1 ? local / P.tiles : 0;
+    local -= r.b * P.tiles;
+    if (P.sym) {
+        r.tm = 0;
+        for (int left = P.ntn; local >= left; --left, ++r.tm) local -= left;   // row tm has ntn - tm tiles
+        r.tn = r.tm + local;
+    } else if (P.m_fast) {
         r.tn = local / P.ntm;
         r.tm = local - r.tn * P.ntm;
     } else {
         r.tm = local / P.ntn;
         r.tn = local - r.tm * P.ntn;
     }
+    r.half = min(kMmHalf, ((P.N - r.tn * kMmTile + 31) & ~31) >> 1);
     const int total = P.nkb * P.parts;
     r.kb0 = r.split * P.kb_per;
     r.kb1 = min(total, r.kb0 + P.kb_per);
@@ -265,26 +288,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             for (int n = 0, u; (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
                 const MmUnit U = mm_unit(G, u);
                 const MmProb &P = G.p[U.q];
-                const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * kMmTile + (int)rank * kMmHalf;
+                const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * kMmTile + (int)rank * U.half;
+                const bool two = !P.b_mn || U.half > 64;   // B's half needs both slices (a K-major box is whole)
+                const uint32_t bytes = 2 * (kMmOperand + (two ? kMmOperand : kMmSlice));   // both CTAs' halves
                 for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
                     const int s = it % kMmStages;
                     const uint32_t ph = (it / kMmStages) & 1;
                     if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
-                    if (rank == 0) mbar_expect_tx(&S.full[s], 4 * kMmOperand);   // both CTAs' halves
+                    if (rank == 0) mbar_expect_tx(&S.full[s], bytes);
                     const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
-                    const int seg = kc / P.nkb, k = (kc - seg * P.nkb) * kMmBK;
-                    const int oa = seg == 2 ? P.lo_a : 0, ob = seg == 1 ? P.lo_b : 0;
+                    int seg = kc / P.nkb;
+                    const int k = (kc - seg * P.nkb) * kMmBK;
+                    if (seg == 1 && P.b_whole) seg = 2;
+                    const int za = U.b * P.za + (seg == 2 ? 1 : 0), zb = U.b * P.zb + (seg == 1 ? 1 : 0);
                     if (P.a_mn) {
-                        tma_load_2d_pair(S.A[s], &P.mA, i0, k + oa, bar);
-                        tma_load_2d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k + oa, bar);
+                        tma_load_3d_pair(S.A[s], &P.mA, i0, k, za, bar);
+                        tma_load_3d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k, za, bar);
                     } else {
-                        tma_load_2d_pair(S.A[s], &P.mA, k, i0 + oa, bar);
+                        tma_load_3d_pair(S.A[s], &P.mA, k, i0, za, bar);
                     }
                     if (P.b_mn) {
-                        tma_load_2d_pair(S.B[s], &P.mB, j0, k + ob, bar);
-                        tma_load_2d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k + ob, bar);
+                        tma_load_3d_pair(S.B[s], &P.mB, j0, k, zb, bar);
+                        if (two) tma_load_3d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k, zb, bar);
                     } else {
-                        tma_load_2d_pair(S.B[s], &P.mB, k, j0 + ob, bar);
+                        tma_load_3d_pair(S.B[s], &P.mB, k, j0, zb, bar);
                     }
                     pend |= 1u << s;
                     pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
@@ -317,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 if (!mbar_wait(&S.acce[ab], aph ^ 1, abort, err, 2)) break;
                 tc_fence_after();
                 const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
-                const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn);
+                const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn, 2 * U.half);
                 const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
                 // 16 k: 32 bytes along a K-major row, or two 8-row groups (2048 bytes) of an MN-major slice
                 const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
@@ -375,23 +402,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     }
 }
 
-// Host: an operand stored as rows of `cols` elements with `pitch` elements between rows.  K-major: a row is an i (or j)
-// and the box is 64 k x 128 rows; MN-major: a row is a k and the box is 64 i x 64 k rows.
-inline bool mm_operand(CUtensorMap *map, bool bf16, bool mn_major, const void *base, long rows, long cols, long pitch)
+// Host: an operand stored as `planes` planes of `rows` rows of `cols` elements, `pitch` elements between rows and
+// `plane` between planes.  K-major: a row is an i (or j) and the box is 64 k x 128 rows; MN-major: a row is a k and the
+// box is 64 i x 64 k rows.  Everything outside reads as zero.
+inline bool mm_operand(CUtensorMap *map, bool bf16, bool mn_major, const void *base, long rows, long cols, long pitch,
+                       long planes = 1, long plane = 0)
 {
-    return tmap_encode_2d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols,
-                          rows, pitch * 2, 64, mn_major ? kMmBK : kMmHalf);
+    return tmap_encode_3d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols,
+                          rows, planes, pitch * 2, (plane ? plane : pitch * rows) * 2, 64, mn_major ? kMmBK : kMmHalf);
 }
 
 // Host: tiles and k ranges of a problem whose k blocks are cut into (at most) `splits` ranges.
-inline void mm_plan(MmProb &P, int M, int N, long K, int parts, bool m_fast, int unit0, int splits)
+inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int splits, int parts = 1, int batch = 1,
+                    bool sym = false)
 {
     P.M = M;
     P.N = N;
     P.parts = parts;
+    P.batch = batch;
+    P.sym = sym ? 1 : 0;
     P.nkb = (int)((K + kMmBK - 1) / kMmBK);
     P.ntm = (M + kMmTile - 1) / kMmTile;
     P.ntn = (N + kMmTile - 1) / kMmTile;
+    P.tiles = sym ? P.ntn * (P.ntn + 1) / 2 : P.ntm * P.ntn;
     P.m_fast = m_fast ? 1 : 0;
     P.unit0 = unit0;
     const int total = P.nkb * parts;
@@ -406,7 +439,7 @@ inline cudaError_t mm_pairs(int *pairs)
     *pairs = sms / 2 > 0 ? sms / 2 : 1;
     return e;
 }
-inline int mm_units(const MmProb &P) { return P.ntm * P.ntn * P.splits; }
+inline int mm_units(const MmProb &P) { return P.tiles * P.batch * P.splits; }
 
 template <bool kBf16, int kMaxProbs, class Epi>
 inline cudaError_t mm_launch(const MmBatch<kMaxProbs> &G, const typename Epi::Params &E, cudaStream_t s)

@@ -1,0 +1,762 @@
+// Orthogonalised updates of latent factors: the Newton-Schulz iteration of the
+// Muon optimiser (Jordan et al., "Muon: An optimizer for hidden layers in
+// neural networks", 2024) for many matrices at once.
+//
+//     X = G / (|G|_F + eps),   `steps` times:  X <- a X + X (b A + c A^2),  A = X^T X
+//     (a, b, c) = (3.4445, -4.7750, 2.0315);   on X^T where G is wide
+//
+// For a tall m x n matrix (m >= n; n is the latent rank, m the features) this
+// is X_0 times a polynomial of A_0 = X_0^T X_0, so the long axis is needed
+// twice only, and everything between is n x n:
+//
+//     q_k = a I + b A_k + c A_k^2,   A_{k+1} = A_k q_k^2,   Q_{k+1} = Q_k q_k,   X_steps = X_0 Q_steps
+//
+// 2 m n^2 (half of it by symmetry) + 2 m n^2 + steps * 4 * 2 n^3 flops instead
+// of steps * (4 m n^2 + 2 n^3).  All these n x n matrices are polynomials of
+// A_0: symmetric, and they commute, so only tiles on and above the diagonal
+// are computed and either orientation may feed the tensor cores.
+//
+// Precision.  The small singular values of an update are what the iteration
+// blows up (by up to a^steps = 485), and in A_0 they are squared, so an error
+// of 2^-12 in A (one binary16 rounding) would move them by percents.  Every
+// operand is therefore a pair of binary16 halves, hi + lo, 22 bits, and a
+// product is hi hi + hi lo + lo hi in one float32 accumulator; the error of the
+// result is below 2e-4 of its norm also for spectra that fall off by 1e4
+// (a rounding of the bfloat16 result itself is 1.7e-3).  Scales are powers of
+// two that keep the halves clear of binary16's ends: G is scaled to root mean
+// square 1 (its largest entry is then at most sqrt(m n)), A, q and A q by 2^13
+// (their eigenvalues stay below 3.5), Q_k by what a^k leaves.
+// bfloat16 G is scaled by a power of two, which makes its high half exact and
+// its low half zero: one product for A_0 instead of three, two for X_0 Q.
+//
+// Ranks up to 64 run the n x n part in one block per matrix, in float32 FMAs;
+// larger ranks as launches over all matrices (three per step), on CTA pairs.
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "lb_mm.cuh"
+#include "littlebit_train.h"
+
+namespace lb {
+namespace {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr int kMostMats = 64, kMostGroups = 8;   // of one set of launches
+constexpr int kNormBlocks = 128;                 // blocks (and partial sums) a matrix has at most
+constexpr int kSmallN = 64;
+constexpr float kSA = 8192.0f;                   // scale of A, q and A q
+constexpr int kMaxSteps = 10;
+
+// One matrix as the elementwise kernels see it.
+struct Mat {
+    const void *G;
+    __half *X;            // [1 or 2 planes][rows][pitch]
+    int rows, cols, pitch;
+    int nblocks;          // blocks of the norm
+};
+struct Mats {
+    Mat m[kMostMats];
+    int n, bf16;
+    float eps;
+    double *sums;         // [n][kNormBlocks]
+    float2 *scal;         // [n]: (kappa, kappa^2 * kSA), X_0 = kappa * (scaled G)
+};
+
+__device__ __forceinline__ float load_g(const void *G, size_t i, int bf16)
+{
+    return bf16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t *>(G)[i]) : reinterpret_cast<const float *>(G)[i];
+}
+
+// Partial sums of squares in binary64 (squares of float32 neither overflow nor vanish there).
+__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Mats P)
+{
+    const Mat &m = P.m[blockIdx.y];
+    if ((int)blockIdx.x >= m.nblocks) return;
+    const size_t n = (size_t)m.rows * m.cols;
+    const size_t step = (size_t)m.nblocks * 256;
+    double s = 0.0;
+    if (!P.bf16 && ((uintptr_t)m.G & 15) == 0) {
+        const size_t nv = n / 4;
+#pragma unroll 4
+        for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nv; i += step) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(m.G) + i);
+            s += ((double)v.x * v.x + (double)v.y * v.y) + ((double)v.z * v.z + (double)v.w * v.w);
+        }
+        if (blockIdx.x == 0 && threadIdx.x < n % 4) {
+            const double v = reinterpret_cast<const float *>(m.G)[nv * 4 + threadIdx.x];
+            s += v * v;
+        }
+    } else {
+#pragma unroll 4
+        for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+            const double v = load_g(m.G, i, P.bf16);
+            s += v * v;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    __shared__ double w[8];
+    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i) s += w[i];
+        P.sums[blockIdx.y * kNormBlocks + blockIdx.x] = s;
+    }
+}
+
+__device__ __forceinline__ void halves(float x, __half &hi, __half &lo)
+{
+    hi = __float2half_rn(x);
+    lo = __float2half_rn(x - __half2float(hi));
+}
+
+// X = G scaled to root mean square about 1, as binary16 halves.
+__global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats P)
+{
+    const Mat &m = P.m[blockIdx.y];
+    if ((int)blockIdx.x >= m.nblocks) return;
+    __shared__ float sc;
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+        for (int i = threadIdx.x; i < m.nblocks; i += 32) s += P.sums[blockIdx.y * kNormBlocks + i];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(s);
+            double c = fmin(sqrt((double)m.rows * m.cols), 32768.0) / norm;
+            if (P.bf16) c = exp2(floor(log2(c)));
+            if (c > 0x1p126) c = 0x1p126;                    // also a zero matrix
+            sc = (float)c;
+            if (blockIdx.x == 0) {
+                const double kappa = 1.0 / (c * (norm + (double)P.eps));
+                P.scal[blockIdx.y] = norm == 0.0 ? make_float2(0.0f, 0.0f)
+                                                 : make_float2((float)kappa, (float)(kappa * kappa * kSA));
+            }
+        }
+    }
+    __syncthreads();
+    const float c = sc;
+    const int nv = m.pitch / 8;
+    const size_t plane = (size_t)m.rows * m.pitch, total = (size_t)m.rows * nv;
+    const bool wide_loads = !P.bf16 && m.cols % 4 == 0 && ((uintptr_t)m.G & 15) == 0;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)m.nblocks * 256) {
+        const size_t row = i / nv;
+        const int col = (int)(i - row * nv) * 8;
+        const size_t g = row * m.cols + col;
+        float x[8];
+        if (wide_loads) {
+            const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(m.G) + g);
+            const float4 u = src[0];
+            const float4 v = col + 4 < m.cols ? src[1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = col + j < m.cols ? load_g(m.G, g + j, P.bf16) : 0.0f;
+        }
+        alignas(16) __half hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) halves(x[j] * c, hi[j], lo[j]);
+        *reinterpret_cast<uint4 *>(m.X + i * 8) = *reinterpret_cast<uint4 *>(hi);
+        if (!P.bf16) *reinterpret_cast<uint4 *>(m.X + plane + i * 8) = *reinterpret_cast<uint4 *>(lo);
+    }
+}
+
+// ---- products
+enum { kPart = 0, kSym = 1, kOut = 2 };
+constexpr int kMostProbs = 2 * kMostGroups;
+struct OrthProb {
+    CUtensorMap mD;       // kPart: float32 [ranges * batch][n][pn]
+    int kind;
+    int pn;               // row pitch of the n x n arrays
+    int first;            // index of the batch's first matrix
+    float alpha, beta, gamma;   // kSym: alpha * product + beta * C + gamma * I;  kOut: alpha * kappa * product
+    const __half *C;      // [batch][2][n][pn], or null
+    __half *D;
+    int ldo;              // kOut: columns of the output
+};
+struct OrthEpi {
+    struct Params {
+        OrthProb p[kMostProbs];
+        uint16_t *out[kMostMats];
+        const float2 *scal;
+    };
+    static __device__ __forceinline__ void run(const Params &E, const MmBatch<kMostProbs> &G, const MmUnit &U,
+                                               const MmTileCtx &T, bool &stored)
+    {
+        const MmProb &P = G.p[U.q];
+        if (T.row0 >= P.M) return;
+        const OrthProb &O = E.p[U.q];
+        const int row = T.row0 + T.lane, cols = min(kMmTile, P.N - T.col0);
+        uint32_t v[32];
+        if (O.kind == kPart) {
+            const int z = U.split * P.batch + U.b;
+            for (int c = 0; c < cols; c += 32) {
+                tmem_ld32(T.tmem + c, v);
+                if (stored) {
+                    if (T.lane == 0) tma_store_wait_read();
+                    __syncwarp();
+                }
+                stored = true;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sts128(T.st + sw128(T.lane, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                fence_proxy_async();
+                __syncwarp();
+                if (T.lane == 0) tma_store_3d(&O.mD, T.col0 + c, T.row0, z, T.st);
+            }
+            return;
+        }
+        if (O.kind == kOut) {
+            uint16_t *const base = E.out[O.first + U.b];
+            uint16_t *dst = base + (size_t)row * O.ldo + T.col0;
+            const float f = O.alpha * E.scal[O.first + U.b].x;
+            const bool vec = O.ldo % 8 == 0 && ((uintptr_t)base & 15) == 0;
+            for (int c = 0; c < cols; c += 32) {
+                tmem_ld32(T.tmem + c, v);
+                if (row >= P.M) continue;
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
+                        : "=r"(w[i])
+                        : "f"(__uint_as_float(v[2 * i + 1]) * f), "f"(__uint_as_float(v[2 * i]) * f));
+                if (vec) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + 8 * i < cols)
+                            *reinterpret_cast<uint4 *>(dst + c + 8 * i) =
+                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < cols) dst[c + i] = (uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+                }
+            }
+            return;
+        }
+        // an n x n matrix, both triangles
+        const size_t plane = (size_t)P.N * O.pn;
+        __half *D = O.D + (size_t)U.b * 2 * plane;
+        const __half *C = O.C ? O.C + (size_t)U.b * 2 * plane : nullptr;
+        const bool mirror = U.tm != U.tn;
+        for (int c = 0; c < cols; c += 32) {
+            tmem_ld32(T.tmem + c, v);
+            if (row >= P.M) continue;
+            alignas(16) __half hi[32], lo[32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = T.col0 + c + 8 * i;
+                alignas(16) __half ch[8], cl[8];
+                const bool in = col < O.pn;
+                if (C && in) {
+                    *reinterpret_cast<uint4 *>(ch) = *reinterpret_cast<const uint4 *>(C + (size_t)row * O.pn + col);
+                    *reinterpret_cast<uint4 *>(cl) = *reinterpret_cast<const uint4 *>(C + plane + (size_t)row * O.pn + col);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float x = __uint_as_float(v[8 * i + j]) * O.alpha;
+                    if (C && in) x += O.beta * (__half2float(ch[j]) + __half2float(cl[j]));
+                    if (col + j == row) x += O.gamma;
+                    halves(x, hi[8 * i + j], lo[8 * i + j]);
+                }
+                if (in) {
+                    *reinterpret_cast<uint4 *>(D + (size_t)row * O.pn + col) = *reinterpret_cast<uint4 *>(hi + 8 * i);
+                    *reinterpret_cast<uint4 *>(D + plane + (size_t)row * O.pn + col) = *reinterpret_cast<uint4 *>(lo + 8 * i);
+                }
+            }
+            if (mirror) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < cols) {
+                        const size_t at = (size_t)(T.col0 + c + i) * O.pn + row;
+                        D[at] = hi[i];
+                        D[plane + at] = lo[i];
+                    }
+            }
+        }
+    }
+};
+
+// ---- A_0 from the Gram product's partial sums (tiles on and above the diagonal), n > 64: 32 x 32 blocks
+struct GroupArg {
+    const float *part;    // [ranges][batch][n][pn]
+    __half *A;            // [batch][2][n][pn]
+    int n, pn, ranges, batch, first, b0;   // b0: first block row of this group in the grid
+};
+struct Groups {
+    GroupArg g[kMostGroups];
+    int n;
+    const float2 *scal;
+};
+
+__device__ __forceinline__ float part_sum(const GroupArg &g, int b, int i, int j)
+{
+    if (i / kMmTile > j / kMmTile) {   // below the diagonal tiles: the mirrored element
+        const int t = i;
+        i = j;
+        j = t;
+    }
+    const size_t plane = (size_t)g.n * g.pn;
+    const float *p = g.part + (size_t)b * plane + (size_t)i * g.pn + j;
+    float s = 0.0f;
+    for (int r = 0; r < g.ranges; ++r) s += p[(size_t)r * g.batch * plane];
+    return s;
+}
+
+__global__ void __launch_bounds__(256) gram_kernel(const __grid_constant__ Groups P)
+{
+    int q = 0;
+    for (int i = 1; i < P.n; ++i)
+        if ((int)blockIdx.y >= P.g[i].b0) q = i;
+    const GroupArg &g = P.g[q];
+    const int b = blockIdx.y - g.b0, nb = (g.n + 31) / 32;
+    int ti = 0, t = blockIdx.x;
+    if (t >= nb * (nb + 1) / 2) return;
+    for (int left = nb; t >= left; --left, ++ti) t -= left;
+    const int tj = ti + t;
+    const float f = P.scal[g.first + b].y;
+    __shared__ float tile[32][33];
+    const size_t plane = (size_t)g.n * g.pn;
+    __half *A = g.A + (size_t)b * 2 * plane;
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+    for (int r = y; r < 32; r += 8) {
+        const int i = ti * 32 + r, j = tj * 32 + x;
+        const float s = i < g.n && j < g.n ? part_sum(g, b, i, j) * f : 0.0f;
+        tile[r][x] = s;
+        if (i < g.n && j < g.n) {
+            __half hi, lo;
+            halves(s, hi, lo);
+            A[(size_t)i * g.pn + j] = hi;
+            A[plane + (size_t)i * g.pn + j] = lo;
+        }
+    }
+    if (ti == tj) return;
+    __syncthreads();
+    for (int r = y; r < 32; r += 8) {
+        const int i = tj * 32 + r, j = ti * 32 + x;
+        if (i < g.n && j < g.n) {
+            __half hi, lo;
+            halves(tile[x][r], hi, lo);
+            A[(size_t)i * g.pn + j] = hi;
+            A[plane + (size_t)i * g.pn + j] = lo;
+        }
+    }
+}
+
+// ---- n <= 64: the whole polynomial in one block, float32
+constexpr int kSmallP = 68;   // row pitch of the shared matrices
+// C = X Y for symmetric X (row k of X serves as its column k); thread (ty, tx) holds C[4 ty ..][4 tx ..]
+__device__ __forceinline__ void small_mul(const float *X, const float *Y, int n, int ty, int tx, float (&c)[4][4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+    for (int k = 0; k < n; ++k) {
+        const float4 x = *reinterpret_cast<const float4 *>(X + k * kSmallP + 4 * ty);
+        const float4 y = *reinterpret_cast<const float4 *>(Y + k * kSmallP + 4 * tx);
+        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+    }
+}
+
+__device__ __forceinline__ void small_put(float *D, int ty, int tx, const float (&c)[4][4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(D + (4 * ty + i) * kSmallP + 4 * tx) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+}
+
+__global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *A = sm, *q = A + 64 * kSmallP, *T = q + 64 * kSmallP, *Q = T + 64 * kSmallP;
+    int w = 0;
+    for (int i = 1; i < P.n; ++i)
+        if ((int)blockIdx.x >= P.g[i].b0) w = i;
+    const GroupArg &g = P.g[w];
+    const int b = blockIdx.x - g.b0, n = g.n, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const float f = P.scal[g.first + b].y * (1.0f / kSA);
+    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+        const int i = e >> 6, j = e & 63;
+        A[i * kSmallP + j] = i < n && j < n ? part_sum(g, b, i, j) * f : 0.0f;
+    }
+    __syncthreads();
+    const bool mine = 4 * ty < n && 4 * tx < n;
+    float c[4][4];
+    for (int k = 0; k < steps; ++k) {
+        if (mine) {
+            small_mul(A, A, n, ty, tx, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    c[i][j] = kC * c[i][j] + kB * A[(4 * ty + i) * kSmallP + 4 * tx + j] +
+                              (4 * ty + i == 4 * tx + j ? kA : 0.0f);
+            small_put(q, ty, tx, c);
+            if (k == 0) small_put(Q, ty, tx, c);
+        }
+        __syncthreads();
+        if (k > 0) {
+            if (mine) small_mul(Q, q, n, ty, tx, c);
+            __syncthreads();
+            if (mine) small_put(Q, ty, tx, c);
+        }
+        if (k + 1 < steps) {
+            if (mine) {
+                small_mul(A, q, n, ty, tx, c);
+                small_put(T, ty, tx, c);
+            }
+            __syncthreads();
+            if (mine) {
+                small_mul(T, q, n, ty, tx, c);
+                small_put(A, ty, tx, c);
+            }
+        }
+        __syncthreads();
+    }
+    const size_t plane = (size_t)n * g.pn;
+    __half *D = g.A + (size_t)b * 2 * plane;
+    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+        const int i = e >> 6, j = e & 63;
+        if (i < n && j < n) {
+            __half hi, lo;
+            halves(Q[i * kSmallP + j] * q_scale, hi, lo);
+            D[(size_t)i * g.pn + j] = hi;
+            D[plane + (size_t)i * g.pn + j] = lo;
+        }
+    }
+}
+
+// ---- host
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+
+// Matrices of one shape, consecutive in the order of a set of launches.
+struct Group {
+    int rows, cols, m, n, pn, pitch, first, batch, ranges;
+    size_t X, part, A, q, T, Q0, Q1;   // workspace offsets; part shares its place with q, T, Q0 and Q1
+    bool wide;
+};
+struct Chunk {
+    std::vector<int> order;
+    std::vector<Group> groups;
+    size_t sums, scal, bytes;
+};
+
+double cost_of(int r, int c)
+{
+    const double n = std::min(r, c), m = std::max(r, c);
+    return n * n * (4 * m + 20 * n);
+}
+
+// Sets of at most kMostMats matrices and kMostGroups shapes, the longest units first in each.
+void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int count, bool bf16)
+{
+    std::vector<int> idx(count);
+    for (int i = 0; i < count; ++i) idx[i] = i;
+    std::sort(idx.begin(), idx.end(), [&](int a, int b) {
+        const int na = std::min(rows[a], cols[a]), nb = std::min(rows[b], cols[b]);
+        if (na != nb) return na > nb;
+        if (rows[a] != rows[b]) return rows[a] > rows[b];
+        if (cols[a] != cols[b]) return cols[a] > cols[b];
+        return a < b;
+    });
+    for (int at = 0; at < count;) {
+        Chunk C;
+        while (at < count && (int)C.order.size() < kMostMats) {
+            const int i = idx[at];
+            if (C.groups.empty() || C.groups.back().rows != rows[i] || C.groups.back().cols != cols[i]) {
+                if ((int)C.groups.size() == kMostGroups) break;
+                Group g;
+                memset(&g, 0, sizeof(g));
+                g.rows = rows[i];
+                g.cols = cols[i];
+                g.wide = rows[i] < cols[i];
+                g.m = std::max(rows[i], cols[i]);
+                g.n = std::min(rows[i], cols[i]);
+                g.pn = (g.n + 7) & ~7;
+                g.pitch = (cols[i] + 7) & ~7;
+                g.first = (int)C.order.size();
+                C.groups.push_back(g);
+            }
+            ++C.groups.back().batch;
+            C.order.push_back(i);
+            ++at;
+        }
+        // ranges of the Gram products: units of about a quarter of a pair's share, at least 24 k blocks (6 us)
+        const int parts = bf16 ? 1 : 3;
+        double total = 0.0;
+        for (const Group &g : C.groups) {
+            const double nt = (g.n + kMmTile - 1) / kMmTile;
+            total += nt * (nt + 1) / 2 * g.batch * parts * ((g.m + kMmBK - 1) / kMmBK);
+        }
+        const long unit = std::max(24L, (long)(total / (74 * 4)));
+        size_t o = 0;
+        auto take = [&](size_t b) {
+            const size_t r = o;
+            o = up256(o + b);
+            return r;
+        };
+        C.sums = take(C.order.size() * kNormBlocks * sizeof(double));
+        C.scal = take(C.order.size() * sizeof(float2));
+        for (Group &g : C.groups) {
+            const long k = (long)parts * ((g.m + kMmBK - 1) / kMmBK);
+            g.ranges = (int)std::min<long>(64, (k + unit - 1) / unit);
+            const long per = (k + g.ranges - 1) / g.ranges;
+            g.ranges = (int)((k + per - 1) / per);
+            const size_t nn = (size_t)g.batch * 2 * g.n * g.pn * 2;
+            g.X = take((size_t)g.batch * (bf16 ? 1 : 2) * g.rows * g.pitch * 2);
+            g.A = take(nn);
+            g.part = o;
+            g.q = take(nn);
+            g.T = take(nn);
+            g.Q0 = take(nn);
+            g.Q1 = take(nn);
+            o = std::max(o, up256(g.part + (size_t)g.ranges * g.batch * g.n * g.pn * 4));
+        }
+        C.bytes = o;
+        out.push_back(std::move(C));
+    }
+}
+
+float q_scale_after(int k) { return exp2f(floorf(log2f(50000.0f / powf(kA, (float)k)))); }
+
+lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps, float eps, uint16_t *const *Os,
+                     unsigned char *ws, cudaStream_t s, int *launches)
+{
+    Mats M;
+    memset(&M, 0, sizeof(M));
+    M.n = (int)C.order.size();
+    M.bf16 = bf16 ? 1 : 0;
+    M.eps = eps;
+    M.sums = (double *)(ws + C.sums);
+    M.scal = (float2 *)(ws + C.scal);
+    int most_blocks = 1;
+    for (const Group &g : C.groups)
+        for (int b = 0; b < g.batch; ++b) {
+            Mat &m = M.m[g.first + b];
+            m.G = Gs[C.order[g.first + b]];
+            m.X = (__half *)(ws + g.X) + (size_t)b * (bf16 ? 1 : 2) * g.rows * g.pitch;
+            m.rows = g.rows;
+            m.cols = g.cols;
+            m.pitch = g.pitch;
+            const size_t n = (size_t)g.rows * g.cols;
+            m.nblocks = (int)std::min<size_t>(kNormBlocks, (n + 8191) / 8192);
+            most_blocks = std::max(most_blocks, m.nblocks);
+        }
+    norm_kernel<<<dim3(most_blocks, M.n), 256, 0, s>>>(M);
+    split_kernel<<<dim3(most_blocks, M.n), 256, 0, s>>>(M);
+    *launches += 2;
+
+    MmBatch<kMostProbs> B;
+    OrthEpi::Params E;
+    memset(&E, 0, sizeof(E));
+    E.scal = M.scal;
+    for (int i = 0; i < M.n; ++i) E.out[i] = Os[C.order[i]];
+    const int parts = bf16 ? 1 : 3, xz = bf16 ? 1 : 2;
+    bool ok = true;
+    auto begin = [&]() { memset(&B, 0, sizeof(B)); };
+    auto launch = [&]() -> cudaError_t {
+        if (B.n == 0) return cudaSuccess;
+        ++*launches;
+        return mm_launch<false, kMostProbs, OrthEpi>(B, E, s);
+    };
+    cudaError_t e;
+
+    // A_0: both operands are X, contracted over the long axis
+    begin();
+    for (const Group &g : C.groups) {
+        MmProb &P = B.p[B.n];
+        OrthProb &O = E.p[B.n];
+        mm_plan(P, g.n, g.n, g.m, false, B.nunits, g.ranges, parts, g.batch, true);
+        P.a_mn = P.b_mn = g.wide ? 0 : 1;
+        P.za = P.zb = xz;
+        ok = ok && mm_operand(&P.mA, false, P.a_mn, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
+        P.mB = P.mA;
+        O.kind = kPart;
+        ok = ok && tmap_encode_3d(&O.mD, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + g.part, g.pn, g.n,
+                                  (long)g.ranges * g.batch, (long)g.pn * 4, (long)g.n * g.pn * 4, 32, 32);
+        B.nunits += mm_units(P);
+        ++B.n;
+    }
+    if (!ok) return LB_ERR_INVALID_ARG;
+    if ((e = launch()) != cudaSuccess) return status_from(e);
+
+    // the small ranks' polynomials, the others' A_0
+    Groups big, small;
+    memset(&big, 0, sizeof(big));
+    memset(&small, 0, sizeof(small));
+    big.scal = small.scal = M.scal;
+    int bigs = 0, smalls = 0, blocks = 0;
+    for (const Group &g : C.groups) {
+        const bool sm = g.n <= kSmallN;
+        Groups &to = sm ? small : big;
+        GroupArg &a = to.g[to.n++];
+        a.part = (const float *)(ws + g.part);
+        a.A = (__half *)(ws + g.A);
+        a.n = g.n;
+        a.pn = g.pn;
+        a.ranges = g.ranges;
+        a.batch = g.batch;
+        a.first = g.first;
+        a.b0 = sm ? smalls : bigs;
+        (sm ? smalls : bigs) += g.batch;
+        const int nb = (g.n + 31) / 32;
+        if (!sm) blocks = std::max(blocks, nb * (nb + 1) / 2);
+    }
+    if (bigs) {
+        gram_kernel<<<dim3(blocks, bigs), 256, 0, s>>>(big);
+        ++*launches;
+    }
+    if (smalls) {
+        const size_t smem = 4 * 64 * kSmallP * sizeof(float);
+        if ((e = ensure_dyn_smem((const void *)small_kernel, smem)) != cudaSuccess) return status_from(e);
+        small_kernel<<<smalls, 256, smem, s>>>(small, steps, q_scale_after(steps));
+        ++*launches;
+    }
+
+    // n > 64: three launches a step
+    auto square = [&](const Group &g, size_t x, size_t y, size_t d, float alpha, float beta, float gamma, size_t c) {
+        MmProb &P = B.p[B.n];
+        OrthProb &O = E.p[B.n];
+        mm_plan(P, g.n, g.n, g.n, false, B.nunits, 1, 3, g.batch, true);
+        P.za = P.zb = 2;
+        ok = ok && mm_operand(&P.mA, false, false, ws + x, g.n, g.n, g.pn, 2L * g.batch) &&
+             mm_operand(&P.mB, false, false, ws + y, g.n, g.n, g.pn, 2L * g.batch);
+        O.kind = kSym;
+        O.pn = g.pn;
+        O.first = g.first;
+        O.alpha = alpha;
+        O.beta = beta;
+        O.gamma = gamma;
+        O.C = c ? (const __half *)(ws + c) : nullptr;
+        O.D = (__half *)(ws + d);
+        B.nunits += mm_units(P);
+        ++B.n;
+    };
+    for (int k = 0; bigs && k < steps; ++k) {
+        begin();   // q = a I + b A + c A^2 (the first is Q_1)
+        for (const Group &g : C.groups)
+            if (g.n > kSmallN) square(g, g.A, g.A, k ? g.q : g.Q0, kC / kSA, kB, kA * kSA, g.A);
+        if (!ok) return LB_ERR_INVALID_ARG;
+        if ((e = launch()) != cudaSuccess) return status_from(e);
+        begin();   // A q, and Q q
+        for (const Group &g : C.groups) {
+            if (g.n <= kSmallN) continue;
+            const size_t q = k ? g.q : g.Q0;
+            if (k + 1 < steps) square(g, g.A, q, g.T, 1.0f / kSA, 0.0f, 0.0f, 0);
+            if (k)
+                square(g, k & 1 ? g.Q0 : g.Q1, q, k & 1 ? g.Q1 : g.Q0,
+                       q_scale_after(k + 1) / ((k == 1 ? kSA : q_scale_after(k)) * kSA), 0.0f, 0.0f, 0);
+        }
+        if (!ok) return LB_ERR_INVALID_ARG;
+        if ((e = launch()) != cudaSuccess) return status_from(e);
+        if (k + 1 == steps) break;
+        begin();   // A q q
+        for (const Group &g : C.groups)
+            if (g.n > kSmallN) square(g, g.T, k ? g.q : g.Q0, g.A, 1.0f / kSA, 0.0f, 0.0f, 0);
+        if (!ok) return LB_ERR_INVALID_ARG;
+        if ((e = launch()) != cudaSuccess) return status_from(e);
+    }
+
+    // the update: X Q, or Q X of a wide matrix
+    begin();
+    for (const Group &g : C.groups) {
+        MmProb &P = B.p[B.n];
+        OrthProb &O = E.p[B.n];
+        const bool sm = g.n <= kSmallN;
+        const size_t Q = sm ? g.A : (steps - 1) & 1 ? g.Q1 : g.Q0;
+        mm_plan(P, g.rows, g.cols, g.n, false, B.nunits, 1, bf16 ? 2 : 3, g.batch);
+        CUtensorMap mQ, mX;
+        ok = ok && mm_operand(&mQ, false, false, ws + Q, g.n, g.n, g.pn, 2L * g.batch) &&
+             mm_operand(&mX, false, g.wide, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
+        P.mA = g.wide ? mQ : mX;
+        P.mB = g.wide ? mX : mQ;
+        P.b_mn = g.wide ? 1 : 0;
+        P.b_whole = g.wide ? 1 : 0;
+        P.za = g.wide ? 2 : xz;
+        P.zb = g.wide ? xz : 2;
+        O.kind = kOut;
+        O.first = g.first;
+        O.alpha = 1.0f / (!sm && steps == 1 ? kSA : q_scale_after(steps));
+        O.ldo = g.cols;
+        B.nunits += mm_units(P);
+        ++B.n;
+    }
+    if (!ok) return LB_ERR_INVALID_ARG;
+    if ((e = launch()) != cudaSuccess) return status_from(e);
+    return status_from(cudaGetLastError());
+}
+
+bool orth_shapes_ok(const int *rows, const int *cols, int n)
+{
+    if (n < 0 || (n > 0 && (!rows || !cols))) return false;
+    for (int i = 0; i < n; ++i)
+        if (rows[i] < 1 || cols[i] < 1) return false;
+    return true;
+}
+
+}  // namespace
+
+lb_status orth_status(cudaStream_t s) { return mm_status(s); }
+
+}  // namespace lb
+
+using namespace lb;
+
+extern "C" size_t lb_orthogonalise_workspace_bytes(const int *rows, const int *cols, int n, int dtype)
+{
+    if (!orth_shapes_ok(rows, cols, n) || (dtype != LB_F32 && dtype != LB_BF16)) return 0;
+    try {
+        std::vector<Chunk> chunks;
+        orth_chunks(chunks, rows, cols, n, dtype == LB_BF16);
+        size_t most = 0;
+        for (const Chunk &c : chunks) most = std::max(most, c.bytes);
+        return most;
+    } catch (...) {
+        return 0;
+    }
+}
+
+extern "C" lb_status lb_orthogonalise(const void *const *G, int dtype, const int *rows, const int *cols, int n, int steps,
+                                      float eps, uint16_t *const *O, void *workspace, size_t workspace_bytes,
+                                      void *stream)
+{
+    set_launch_count(0);
+    if (!orth_shapes_ok(rows, cols, n) || (dtype != LB_F32 && dtype != LB_BF16) || steps < 1 || !(eps >= 0.0f))
+        return LB_ERR_INVALID_ARG;
+    if (steps > kMaxSteps) return LB_ERR_UNSUPPORTED;
+    if (n == 0) return LB_OK;
+    if (!G || !O || !workspace || misaligned(workspace, 256)) return LB_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        if (!G[i] || !O[i] || misaligned(G[i], dtype == LB_F32 ? 4 : 2) || misaligned(O[i], 2)) return LB_ERR_INVALID_ARG;
+        if (std::min(rows[i], cols[i]) > LB_MAX_RANK || std::max(rows[i], cols[i]) > (1 << 24)) return LB_ERR_UNSUPPORTED;
+    }
+    try {
+        std::vector<Chunk> chunks;
+        orth_chunks(chunks, rows, cols, n, dtype == LB_BF16);
+        for (const Chunk &c : chunks)
+            if (workspace_bytes < c.bytes) return LB_ERR_INVALID_ARG;
+        if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
+        int launches = 0;
+        for (const Chunk &c : chunks) {
+            const lb_status st = orth_chunk(c, G, dtype == LB_BF16, steps, eps, O, (unsigned char *)workspace,
+                                            (cudaStream_t)stream, &launches);
+            if (st != LB_OK) return st;
+        }
+        set_launch_count(launches);
+    } catch (const std::bad_alloc &) {
+        return LB_ERR_OOM;
+    } catch (...) {
+        return LB_ERR_INVALID_ARG;
+    }
+    return LB_OK;
+}

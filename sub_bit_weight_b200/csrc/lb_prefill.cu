@@ -620,6 +620,18 @@ bool tmap_encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, 
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tmap_encode_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, long cols, long rows, long planes,
+                    long pitch_bytes, long plane_bytes, int box_cols, int box_rows)
+{
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch_bytes, (cuuint64_t)plane_bytes};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static cudaError_t get_encoder() { return tmap_encoder_ready(); }
 
 static bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, int cols, int rows,

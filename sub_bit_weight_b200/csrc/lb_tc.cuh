@@ -163,4 +163,8 @@ cudaError_t tmap_encoder_ready();
 bool tmap_encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, long cols, long rows,
                     long pitch_bytes, int box_cols, int box_rows);
 
+// Host: the same for an array [planes][rows][cols], box box_cols x box_rows x 1 (a single plane may have any pitch).
+bool tmap_encode_3d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, long cols, long rows, long planes,
+                    long pitch_bytes, long plane_bytes, int box_cols, int box_rows);
+
 }  // namespace lb

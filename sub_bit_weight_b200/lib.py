@@ -509,6 +509,10 @@ _sig("lb_cross_entropy_forward_workspace_bytes", ctypes.c_size_t, [_i, _i, _i])
 _sig("lb_cross_entropy_forward", _st, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("lb_cross_entropy_gradient_workspace_bytes", ctypes.c_size_t, [_i, _i, _i, _i, _i])
 _sig("lb_cross_entropy_gradient", _st, [_vp, _vp, _vp, _vp] + [_i] * 4 + [_vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("lb_orthogonalise_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(_i)] * 2 + [_i, _i])
+_sig("lb_orthogonalise", _st, [ctypes.POINTER(_vp), _i] + [ctypes.POINTER(_i)] * 2 + [_i, _i, ctypes.c_float,
+                                                                                 ctypes.POINTER(_vp), _vp,
+                                                                                 ctypes.c_size_t, _vp])
 _sig("lb_train_status", _st, [_vp])
 
 
@@ -655,3 +659,32 @@ def lb_cross_entropy_gradient(H: torch.Tensor, W: torch.Tensor, labels: torch.Te
                                               _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream),
                "lb_cross_entropy_gradient")
     return loss, dH, dW
+
+
+def lb_orthogonalise_workspace_bytes(shapes, dtype: torch.dtype = torch.float32) -> int:
+    n = len(shapes)
+    rows, cols = ((_i * max(1, n))(*[s[k] for s in shapes]) for k in (0, 1))
+    return int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, _element(dtype, "dtype")))
+
+
+def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tensor | None = None, stream=None) -> list:
+    """Orthogonalised updates (Newton-Schulz, as the Muon optimiser) of a list of matrices [rows, cols], all float32 or
+    all bfloat16, such as the dU and dV of a block's layers: a list of bfloat16 tensors of the same shapes."""
+    G = list(G)
+    n = len(G)
+    if n == 0:
+        return []
+    for i, t in enumerate(G):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.numel() == 0:
+            raise ValueError(f"G[{i}] must be a matrix with at least one element")
+    dtype = G[0].dtype
+    code = _element(dtype, "G")
+    rows, cols = ((_i * n)(*[t.shape[k] for t in G]) for k in (0, 1))
+    with _On(stream, **{f"G[{i}]": t for i, t in enumerate(G)}) as on:
+        out = [torch.empty(t.shape, dtype=torch.bfloat16, device=on.device) for t in G]
+        need = int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code))
+        ws = _workspace(workspace, need, on)
+        _check(_lib.lb_orthogonalise((_vp * n)(*[_dev(t, dtype, f"G[{i}]") for i, t in enumerate(G)]), code, rows, cols, n,
+                                     int(steps), float(eps), (_vp * n)(*[t.data_ptr() for t in out]),
+                                     _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream), "lb_orthogonalise")
+    return out
