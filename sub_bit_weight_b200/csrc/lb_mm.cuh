@@ -21,7 +21,7 @@
 //
 // A problem is a batch of equal products, its operands arrays [z][row][column].
 // With parts = 3 each operand is a pair of halves (the planes z and z + 1: high
-// and low), and hi * hi + hi * lo + lo * hi runs as one main loop three times as
+// and low), and lo * hi + hi * lo + hi * hi runs as one main loop three times as
 // long; with parts = 2 one operand is whole and only the other has a low half.
 // A problem marked symmetric has only its tiles on and above the diagonal.
 //
@@ -297,10 +297,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                     if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
                     if (rank == 0) mbar_expect_tx(&S.full[s], bytes);
                     const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
-                    int seg = kc / P.nkb;
+                    // low halves first: the accumulator truncates, by what is already in it
+                    const int seg = kc / P.nkb, left = P.parts - 1 - seg;
                     const int k = (kc - seg * P.nkb) * kMmBK;
-                    if (seg == 1 && P.b_whole) seg = 2;
-                    const int za = U.b * P.za + (seg == 2 ? 1 : 0), zb = U.b * P.zb + (seg == 1 ? 1 : 0);
+                    const int la = left == 2 || (left == 1 && P.b_whole), lb = left == 1 && !P.b_whole;
+                    const int za = U.b * P.za + (la ? 1 : 0), zb = U.b * P.zb + (lb ? 1 : 0);
                     if (P.a_mn) {
                         tma_load_3d_pair(S.A[s], &P.mA, i0, k, za, bar);
                         tma_load_3d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k, za, bar);

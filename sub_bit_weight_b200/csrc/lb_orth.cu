@@ -173,9 +173,11 @@ struct OrthProb {
     int kind;
     int pn;               // row pitch of the n x n arrays
     int first;            // index of the batch's first matrix
-    float alpha, beta, gamma;   // kSym: alpha * product + beta * C + gamma * I;  kOut: alpha * kappa * product
-    const __half *C;      // [batch][2][n][pn], or null
+    float alpha, beta;    // kSym: alpha * product + beta * C;  kOut: alpha * kappa * product
+    const __half *C;      // [batch][2][n][pn]
     __half *D;
+    __half *D2;           // null, or the same plus gamma * I
+    float gamma;
     int ldo;              // kOut: columns of the output
 };
 struct OrthEpi {
@@ -238,46 +240,71 @@ struct OrthEpi {
             }
             return;
         }
-        // an n x n matrix, both triangles
+        // A symmetric n x n matrix: every element on or above the diagonal is computed once and written to both its
+        // places.  (The products of a polynomial's factors are symmetric only up to rounding, and a difference between
+        // the triangles would grow by q(0)^2 = 12 a step, twice as fast in its exponent as the matrix itself.)
         const size_t plane = (size_t)P.N * O.pn;
-        __half *D = O.D + (size_t)U.b * 2 * plane;
-        const __half *C = O.C ? O.C + (size_t)U.b * 2 * plane : nullptr;
-        const bool mirror = U.tm != U.tn;
+        const __half *C = O.C + (size_t)U.b * 2 * plane;
         for (int c = 0; c < cols; c += 32) {
             tmem_ld32(T.tmem + c, v);
-            if (row >= P.M) continue;
-            alignas(16) __half hi[32], lo[32];
+            const int col0 = T.col0 + c;
+            if (row >= P.M || col0 + 31 < row) continue;
+            float x[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int col = T.col0 + c + 8 * i;
                 alignas(16) __half ch[8], cl[8];
-                const bool in = col < O.pn;
-                if (C && in) {
-                    *reinterpret_cast<uint4 *>(ch) = *reinterpret_cast<const uint4 *>(C + (size_t)row * O.pn + col);
-                    *reinterpret_cast<uint4 *>(cl) = *reinterpret_cast<const uint4 *>(C + plane + (size_t)row * O.pn + col);
+                const bool in = col0 + 8 * i < O.pn;
+                if (in) {
+                    *reinterpret_cast<uint4 *>(ch) =
+                        *reinterpret_cast<const uint4 *>(C + (size_t)row * O.pn + col0 + 8 * i);
+                    *reinterpret_cast<uint4 *>(cl) =
+                        *reinterpret_cast<const uint4 *>(C + plane + (size_t)row * O.pn + col0 + 8 * i);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    float x = __uint_as_float(v[8 * i + j]) * O.alpha;
-                    if (C && in) x += O.beta * (__half2float(ch[j]) + __half2float(cl[j]));
-                    if (col + j == row) x += O.gamma;
-                    halves(x, hi[8 * i + j], lo[8 * i + j]);
-                }
-                if (in) {
-                    *reinterpret_cast<uint4 *>(D + (size_t)row * O.pn + col) = *reinterpret_cast<uint4 *>(hi + 8 * i);
-                    *reinterpret_cast<uint4 *>(D + plane + (size_t)row * O.pn + col) = *reinterpret_cast<uint4 *>(lo + 8 * i);
+                    const float y = in ? __half2float(ch[j]) + __half2float(cl[j]) : 0.0f;
+                    x[8 * i + j] = fmaf(__uint_as_float(v[8 * i + j]), O.alpha, O.beta * y);
                 }
             }
-            if (mirror) {
+            put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, row, col0, P.N);
+            if (O.D2) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c + i < cols) {
-                        const size_t at = (size_t)(T.col0 + c + i) * O.pn + row;
-                        D[at] = hi[i];
-                        D[plane + at] = lo[i];
-                    }
+                    if (col0 + i == row) x[i] += O.gamma;
+                put(x, O.D2 + (size_t)U.b * 2 * plane, plane, O.pn, row, col0, P.N);
             }
         }
+    }
+    // 32 columns of a row: the elements on or above the diagonal, and their mirror images
+    static __device__ __forceinline__ void put(const float (&x)[32], __half *D, size_t plane, int pn, int row, int col0,
+                                               int n)
+    {
+        alignas(16) __half hi[32], lo[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) halves(x[i], hi[i], lo[i]);
+        if (col0 >= row) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col0 + 8 * i < pn) {
+                    *reinterpret_cast<uint4 *>(D + (size_t)row * pn + col0 + 8 * i) = *reinterpret_cast<uint4 *>(hi + 8 * i);
+                    *reinterpret_cast<uint4 *>(D + plane + (size_t)row * pn + col0 + 8 * i) =
+                        *reinterpret_cast<uint4 *>(lo + 8 * i);
+                }
+        } else {   // the block on the diagonal
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col0 + i >= row && col0 + i < n) {
+                    D[(size_t)row * pn + col0 + i] = hi[i];
+                    D[plane + (size_t)row * pn + col0 + i] = lo[i];
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (col0 + i > row && col0 + i < n) {
+                const size_t at = (size_t)(col0 + i) * pn + row;
+                D[at] = hi[i];
+                D[plane + at] = lo[i];
+            }
     }
 };
 
@@ -367,11 +394,24 @@ __device__ __forceinline__ void small_mul(const float *X, const float *Y, int n,
     }
 }
 
+// blocks on and above the diagonal, written to both places (see OrthEpi)
 __device__ __forceinline__ void small_put(float *D, int ty, int tx, const float (&c)[4][4])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4 *>(D + (4 * ty + i) * kSmallP + 4 * tx) = make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (4 * ty + i <= 4 * tx + j)
+                D[(4 * ty + i) * kSmallP + 4 * tx + j] = D[(4 * tx + j) * kSmallP + 4 * ty + i] = c[i][j];
+}
+
+// c = a D + c
+__device__ __forceinline__ void small_add(const float *D, int ty, int tx, float a, float (&c)[4][4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a, D[(4 * ty + i) * kSmallP + 4 * tx + j], c[i][j]);
 }
 
 __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
@@ -389,7 +429,7 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
         A[i * kSmallP + j] = i < n && j < n ? part_sum(g, b, i, j) * f : 0.0f;
     }
     __syncthreads();
-    const bool mine = 4 * ty < n && 4 * tx < n;
+    const bool mine = ty <= tx && 4 * tx < n;
     float c[4][4];
     for (int k = 0; k < steps; ++k) {
         if (mine) {
@@ -397,26 +437,37 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c[i][j] = kC * c[i][j] + kB * A[(4 * ty + i) * kSmallP + 4 * tx + j] +
-                              (4 * ty + i == 4 * tx + j ? kA : 0.0f);
+                for (int j = 0; j < 4; ++j) c[i][j] *= kC;
+            small_add(A, ty, tx, kB, c);
             small_put(q, ty, tx, c);
-            if (k == 0) small_put(Q, ty, tx, c);
+            if (k == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (4 * ty + i == 4 * tx + j) c[i][j] += kA;
+                small_put(Q, ty, tx, c);
+            }
         }
         __syncthreads();
         if (k > 0) {
-            if (mine) small_mul(Q, q, n, ty, tx, c);
+            if (mine) {
+                small_mul(Q, q, n, ty, tx, c);
+                small_add(Q, ty, tx, kA, c);
+            }
             __syncthreads();
             if (mine) small_put(Q, ty, tx, c);
         }
         if (k + 1 < steps) {
             if (mine) {
                 small_mul(A, q, n, ty, tx, c);
+                small_add(A, ty, tx, kA, c);
                 small_put(T, ty, tx, c);
             }
             __syncthreads();
             if (mine) {
                 small_mul(T, q, n, ty, tx, c);
+                small_add(T, ty, tx, kA, c);
                 small_put(A, ty, tx, c);
             }
         }
@@ -624,7 +675,8 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     }
 
     // n > 64: three launches a step
-    auto square = [&](const Group &g, size_t x, size_t y, size_t d, float alpha, float beta, float gamma, size_t c) {
+    // d = alpha * x y + beta * c
+    auto square = [&](const Group &g, size_t x, size_t y, size_t d, float alpha, float beta, size_t c) -> OrthProb & {
         MmProb &P = B.p[B.n];
         OrthProb &O = E.p[B.n];
         mm_plan(P, g.n, g.n, g.n, false, B.nunits, 1, 3, g.batch, true);
@@ -636,33 +688,42 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         O.first = g.first;
         O.alpha = alpha;
         O.beta = beta;
-        O.gamma = gamma;
-        O.C = c ? (const __half *)(ws + c) : nullptr;
+        O.C = (const __half *)(ws + c);
         O.D = (__half *)(ws + d);
+        O.D2 = nullptr;
         B.nunits += mm_units(P);
         ++B.n;
+        return O;
     };
     for (int k = 0; bigs && k < steps; ++k) {
-        begin();   // q = a I + b A + c A^2 (the first is Q_1)
-        for (const Group &g : C.groups)
-            if (g.n > kSmallN) square(g, g.A, g.A, k ? g.q : g.Q0, kC / kSA, kB, kA * kSA, g.A);
-        if (!ok) return LB_ERR_INVALID_ARG;
-        if ((e = launch()) != cudaSuccess) return status_from(e);
-        begin();   // A q, and Q q
+        begin();   // p = b A + c A^2; the first also gives Q_1 = a I + p
         for (const Group &g : C.groups) {
             if (g.n <= kSmallN) continue;
-            const size_t q = k ? g.q : g.Q0;
-            if (k + 1 < steps) square(g, g.A, q, g.T, 1.0f / kSA, 0.0f, 0.0f, 0);
-            if (k)
-                square(g, k & 1 ? g.Q0 : g.Q1, q, k & 1 ? g.Q1 : g.Q0,
-                       q_scale_after(k + 1) / ((k == 1 ? kSA : q_scale_after(k)) * kSA), 0.0f, 0.0f, 0);
+            OrthProb &O = square(g, g.A, g.A, g.q, kC / kSA, kB, g.A);
+            if (k == 0) {
+                O.D2 = (__half *)(ws + g.Q0);
+                O.gamma = kA * kSA;
+            }
+        }
+        if (!ok) return LB_ERR_INVALID_ARG;
+        if ((e = launch()) != cudaSuccess) return status_from(e);
+        if (k + 1 == steps && k == 0) break;
+        begin();   // T = a A + A p, and Q <- a Q + Q p
+        for (const Group &g : C.groups) {
+            if (g.n <= kSmallN) continue;
+            if (k + 1 < steps) square(g, g.A, g.q, g.T, 1.0f / kSA, kA, g.A);
+            if (k) {
+                const size_t from = k & 1 ? g.Q0 : g.Q1, to = k & 1 ? g.Q1 : g.Q0;
+                const float f = q_scale_after(k + 1) / (k == 1 ? kSA : q_scale_after(k));
+                square(g, from, g.q, to, f / kSA, kA * f, from);
+            }
         }
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
         if (k + 1 == steps) break;
-        begin();   // A q q
+        begin();   // A <- a T + T p
         for (const Group &g : C.groups)
-            if (g.n > kSmallN) square(g, g.T, k ? g.q : g.Q0, g.A, 1.0f / kSA, 0.0f, 0.0f, 0);
+            if (g.n > kSmallN) square(g, g.T, g.q, g.A, 1.0f / kSA, kA, g.T);
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
     }
