@@ -10,11 +10,12 @@
 //
 //   1  z tiles (256 rows x 256 vocabulary entries) on CTA pairs.  The epilogue
 //      takes each row's maximum m and sum of exp(z - m) over the tile (one
-//      thread a row, two passes over tensor memory) and, for the gradient,
+//      thread a row and 128 columns, which it holds in registers) and, for the gradient,
 //      leaves e = 2^15 exp(z - m) in binary16: at most 2^15, exact to 2^-12
 //      down to 2^-29 of the tile's maximum and to 2^-39 of it below that.
 //   2  one block per row and 8192 entries: lse from the tiles' (m, s), then
-//      G = w (e exp(m - lse) 2^-15 - onehot) rounded to bfloat16 over e.
+//      G / max w = w / max w (e exp(m - lse) 2^-15 - onehot), rounded to
+//      bfloat16, over e.
 //   3  dH = G W and dW = G^T H in one launch; G and W (dH) and G and H (dW)
 //      are read in the orientation they are stored in, whichever index is
 //      contracted.
@@ -34,6 +35,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kEScale = 15.0f;        // e is stored times 2^15
+constexpr int kChunk = 16;             // k blocks (1024 k) of logits one accumulator takes, see lb_mm.cuh
 constexpr int kGradCols = 8192;         // entries of a row one block of the second step takes
 constexpr int kRowsDefault = 8192, kRowsMost = 32768;
 
@@ -77,75 +79,87 @@ __device__ __forceinline__ void staging_free(bool &stored, int lane)
     stored = true;
 }
 
-// ---- 1: statistics of a tile of logits (kKeep: and e)
+// ---- 1: statistics of 128 columns of a row of logits (kKeep: and e)
 template <bool kKeep>
 struct LogitEpi {
+    static constexpr bool kManyRegs = true;
     struct Params {
         CUtensorMap mE;            // binary16 [rows][Vp]
         const int64_t *labels;
-        float2 *stat;              // [rows][ntn]: (reference exponent, sum), base 2
+        float2 *stat;              // [rows][nst]: (reference exponent, sum), base 2, of each 128 columns
         float *target;             // [rows]: z of the label
-        int M, V, ntn;
+        int M, V, nst;
     };
-    static __device__ __forceinline__ void run(const Params &E, const MmBatch<1> &, const MmUnit &U, const MmTileCtx &T,
-                                               bool &stored)
+    struct State {
+        float z[kMmHalf];          // the row's logits
+        int at;                    // column of the label, -1 if it is not among them
+    };
+    static __device__ __forceinline__ void begin(const Params &E, const MmProb &, const MmUnit &, const MmTileCtx &T,
+                                                 State &S)
     {
         const int row = T.row0 + T.lane;
-        const int valid = min(kMmTile, E.V - T.col0);   // columns of the tile inside the vocabulary
-        if (T.row0 >= E.M) return;
-        long long lab = row < E.M ? E.labels[row] : -1;
-        const int at = lab >= T.col0 && lab < T.col0 + valid ? (int)(lab - T.col0) : -1;
-        float mx = -INFINITY;
-        uint32_t v[32];
-        for (int c = 0; c < valid; c += 32) {
+        const long long lab = T.cols > 0 && row < E.M ? E.labels[row] : -1;
+        S.at = lab >= T.col0 && lab < T.col0 + T.cols ? (int)(lab - T.col0) : -1;
+    }
+    static __device__ __forceinline__ void take(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &T,
+                                                State &S, bool first, bool, bool &)
+    {
+        if (T.cols == 0) return;
+#pragma unroll
+        for (int c = 0; c < kMmHalf; c += 32) {
+            uint32_t v[32];
             tmem_ld32(T.tmem + c, v);
-            if (c + 32 > valid) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (c + i >= valid) v[i] = 0xff800000u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-            if (at >= c && at < c + 32) {
-                uint32_t z = 0;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z = pick(at - c, i, v[i], z);
-                E.target[row] = __uint_as_float(z);
-            }
+            for (int i = 0; i < 32; ++i)
+                S.z[c + i] = first ? __uint_as_float(v[i]) : S.z[c + i] + __uint_as_float(v[i]);
         }
+    }
+    static __device__ __forceinline__ void end(const Params &E, const MmProb &, const MmUnit &, const MmTileCtx &T,
+                                               State &S, bool &stored)
+    {
+        if (T.cols == 0) return;
+        const int row = T.row0 + T.lane;
+        if (T.cols < kMmHalf) {
+#pragma unroll
+            for (int i = 0; i < kMmHalf; ++i)
+                if (i >= T.cols) S.z[i] = -INFINITY;
+        }
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < kMmHalf; ++i) m[i & 3] = fmaxf(m[i & 3], S.z[i]);
+        if (S.at >= 0) {
+            uint32_t z = 0;
+#pragma unroll
+            for (int i = 0; i < kMmHalf; ++i) z = pick(S.at, i, __float_as_uint(S.z[i]), z);
+            E.target[row] = __uint_as_float(z);
+        }
+        const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         const float ref = fmaf(mx, kLog2e, -kEScale);
-        const float sub = mx == -INFINITY ? 0.0f : ref;   // a tile of nothing but -inf (or NaN): weights 0 (or NaN)
+        const float sub = mx == -INFINITY ? 0.0f : ref;   // nothing but -inf (or NaN): weights 0 (or NaN)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int cols = kKeep ? (valid + 63) & ~63 : (valid + 31) & ~31;
-        for (int c = 0; c < cols; c += 32) {
-            tmem_ld32(T.tmem + c, v);
-            if (c + 32 > valid) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (c + i >= valid) v[i] = 0xff800000u;
-            }
-            float e[32];
+        for (int i = 0; i < kMmHalf; ++i) {
+            S.z[i] = ex2(fmaf(S.z[i], kLog2e, -sub));
+            s[i & 3] += S.z[i];
+        }
+        if (row < E.M)
+            E.stat[(size_t)row * E.nst + T.col0 / kMmHalf] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
+        if (kKeep) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                e[i] = ex2(fmaf(__uint_as_float(v[i]), kLog2e, -sub));
-                s[i & 3] += e[i];
-            }
-            if (kKeep) {
-                const int half = (c >> 5) & 1;   // 32 columns = half of a 128-byte staging row
-                if (half == 0) staging_free(stored, T.lane);
+            for (int c = 0; c < kMmHalf; c += 64) {
+                if (c >= T.cols) break;
+                staging_free(stored, T.lane);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sts128(T.st + sw128(T.lane, half * 4 + i),
-                           make_uint4(pack_h2(e[8 * i], e[8 * i + 1]), pack_h2(e[8 * i + 2], e[8 * i + 3]),
-                                      pack_h2(e[8 * i + 4], e[8 * i + 5]), pack_h2(e[8 * i + 6], e[8 * i + 7])));
-                if (half == 1) {
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (T.lane == 0) tma_store_2d(&E.mE, T.col0 + c - 32, T.row0, T.st);
+                for (int i = 0; i < 8; ++i) {
+                    const float *e = S.z + c + 8 * i;
+                    sts128(T.st + sw128(T.lane, i), make_uint4(pack_h2(e[0], e[1]), pack_h2(e[2], e[3]),
+                                                               pack_h2(e[4], e[5]), pack_h2(e[6], e[7])));
                 }
+                fence_proxy_async();
+                __syncwarp();
+                if (T.lane == 0) tma_store_2d(&E.mE, T.col0 + c, T.row0, T.st);
             }
         }
-        if (row < E.M) E.stat[(size_t)row * E.ntn + U.tn] = make_float2(ref, (s[0] + s[1]) + (s[2] + s[3]));
     }
 };
 
@@ -169,13 +183,13 @@ __device__ __forceinline__ float2 lse_warp(float2 a)
 }
 
 __global__ void __launch_bounds__(256) lse_kernel(const float2 *__restrict__ stat, const float *__restrict__ target,
-                                                  const int64_t *__restrict__ labels, int M, int V, int ntn,
+                                                  const int64_t *__restrict__ labels, int M, int V, int nst,
                                                   float *__restrict__ loss, float *__restrict__ lse)
 {
     const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (row >= M) return;
     float2 a = make_float2(-INFINITY, 0.0f);
-    for (int t = lane; t < ntn; t += 32) a = lse_merge(a, stat[(size_t)row * ntn + t]);
+    for (int t = lane; t < nst; t += 32) a = lse_merge(a, stat[(size_t)row * nst + t]);
     a = lse_warp(a);
     if (lane == 0) {
         const long long lab = labels[row];
@@ -185,11 +199,38 @@ __global__ void __launch_bounds__(256) lse_kernel(const float2 *__restrict__ sta
     }
 }
 
+// The largest finite |weight| of a row that counts (1 if there is none): G is held relative to it, so that with equal
+// weights, a mean, the entries of G are p and p - 1 themselves, and the one that dominates a row, near -1, is rounded
+// hardly at all (w (p - 1) would round by up to 2^-8, the same way in every row).
+__global__ void __launch_bounds__(1024) wref_kernel(const float *__restrict__ weight, const int64_t *__restrict__ labels,
+                                                    int M, int V, float *__restrict__ wref)
+{
+    float m = 0.0f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < M; i += 1024) {
+        const float w = fabsf(weight[i]);
+        const long long lab = labels[i];
+        if (lab >= 0 && lab < V && w < INFINITY) m = fmaxf(m, w);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __shared__ float part[32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = part[threadIdx.x];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (threadIdx.x == 0) *wref = m > 0.0f ? m : 1.0f;
+    }
+}
+
 // ---- 2: G over e, the loss, and (Hc) H with the rows that do not count zeroed, the operand of dW
 __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const float2 *__restrict__ stat,
                                                    const float *__restrict__ target,
                                                    const int64_t *__restrict__ labels,
-                                                   const float *__restrict__ weight, int V, int Vp, int ntn, int D,
+                                                   const float *__restrict__ weight,
+                                                   const float *__restrict__ wref, int V, int Vp, int nst, int D,
                                                    const uint4 *__restrict__ H, uint4 *__restrict__ Hc,
                                                    float *__restrict__ loss)
 {
@@ -208,9 +249,9 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
         if (chunk == 0 && threadIdx.x == 0) loss[row] = 0.0f;
         return;
     }
-    const float2 *st = stat + (size_t)row * ntn;
+    const float2 *st = stat + (size_t)row * nst;
     float2 a = make_float2(-INFINITY, 0.0f);
-    for (int t = threadIdx.x; t < ntn; t += 256) a = lse_merge(a, st[t]);
+    for (int t = threadIdx.x; t < nst; t += 256) a = lse_merge(a, st[t]);
     a = lse_warp(a);
     __shared__ float2 part[8];
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
@@ -218,12 +259,14 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
     a = lse_warp(part[threadIdx.x & 7]);   // every warp: the eight parts, four times over
     a.y *= 0.25f;
     const float lse2 = a.x + log2f(a.y);
-    const float w = weight[row];
-    if (chunk == 0 && threadIdx.x == 0) loss[row] = lse2 * kLn2 - target[row];
+    const float w = weight[row] / *wref, z = target[row];
+    if (chunk == 0 && threadIdx.x == 0) loss[row] = lse2 * kLn2 - z;
+    // the label's entry from the float32 logit: p - 1 of a sure row is far below the rounding of p
+    const float at_label = w * (ex2(fmaf(z, kLog2e, -lse2)) - 1.0f);
 #pragma unroll 4
     for (int i = v0 + threadIdx.x; i < v1; i += 256) {
         const uint4 q = out[i];
-        const float f = w * ex2(st[i >> 5].x - lse2);   // 32 vectors to a tile of 256 entries
+        const float f = w * ex2(st[i >> 4].x - lse2);   // 16 vectors to 128 entries
         const uint32_t in[4] = {q.x, q.y, q.z, q.w};
         float g[8];
 #pragma unroll
@@ -235,7 +278,7 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
         if (lab >> 3 == i) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if ((lab & 7) == j) g[j] -= w;
+                if ((lab & 7) == j) g[j] = at_label;
         }
         out[i] = make_uint4(pack_bf2(g[0], g[1]), pack_bf2(g[2], g[3]), pack_bf2(g[4], g[5]), pack_bf2(g[6], g[7]));
     }
@@ -244,21 +287,29 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
 // ---- 3: the two products
 enum { kOutBf16 = 0, kOutF32 = 1, kOutF32Add = 2 };
 struct ProductEpi {
+    static constexpr bool kManyRegs = false;
     struct Params {
         CUtensorMap mD[2];
         int kind[2];
         int split_rows[2];   // rows between the partial results of consecutive k ranges
+        const float *wref;
     };
-    static __device__ __forceinline__ void run(const Params &E, const MmBatch<2> &G, const MmUnit &U, const MmTileCtx &T,
-                                               bool &stored)
+    struct State {};
+    static __device__ __forceinline__ void begin(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &)
     {
-        const MmProb &P = G.p[U.q];
-        if (T.row0 >= P.M) return;
+    }
+    static __device__ __forceinline__ void end(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &,
+                                               bool &)
+    {
+    }
+    static __device__ __forceinline__ void take(const Params &E, const MmProb &, const MmUnit &U, const MmTileCtx &T,
+                                                State &, bool, bool, bool &stored)
+    {
         const int kind = E.kind[U.q], y = T.row0 + U.split * E.split_rows[U.q];
         const CUtensorMap *map = &E.mD[U.q];
-        const int cols = min(kMmTile, P.N - T.col0);
+        const float f = kind == kOutBf16 ? *E.wref : 1.0f;
         uint32_t v[32];
-        for (int c = 0; c < cols; c += 32) {
+        for (int c = 0; c < T.cols; c += 32) {
             tmem_ld32(T.tmem + c, v);
             if (kind == kOutBf16) {
                 const int half = (c >> 5) & 1;
@@ -268,10 +319,10 @@ struct ProductEpi {
                     uint32_t p[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        p[j] = pack_bf2(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                        p[j] = pack_bf2(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
                     sts128(T.st + sw128(T.lane, half * 4 + i), make_uint4(p[0], p[1], p[2], p[3]));
                 }
-                if (half == 0 && c + 32 < cols) continue;
+                if (half == 0 && c + 32 < T.cols) continue;
                 fence_proxy_async();
                 __syncwarp();
                 if (T.lane == 0) tma_store_2d(map, T.col0 + (c & ~63), y, T.st);
@@ -293,10 +344,12 @@ struct ProductEpi {
     }
 };
 
-// out = bfloat16(sum of n fp32 parts `stride` elements apart), in order; 8 elements a thread
+// out = bfloat16(*wref * sum of n fp32 parts `stride` elements apart), in order; 8 elements a thread
 __global__ void __launch_bounds__(256) round_sum_kernel(const float4 *__restrict__ part, size_t stride4, int n,
-                                                        size_t nvec, uint4 *__restrict__ out)
+                                                        size_t nvec, const float *__restrict__ wref,
+                                                        uint4 *__restrict__ out)
 {
+    const float f = *wref;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nvec; i += (size_t)gridDim.x * 256) {
         float4 a = part[2 * i], b = part[2 * i + 1];
         for (int s = 1; s < n; ++s) {
@@ -304,7 +357,8 @@ __global__ void __launch_bounds__(256) round_sum_kernel(const float4 *__restrict
             a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
             b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
         }
-        out[i] = make_uint4(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w), pack_bf2(b.x, b.y), pack_bf2(b.z, b.w));
+        out[i] = make_uint4(pack_bf2(a.x * f, a.y * f), pack_bf2(a.z * f, a.w * f), pack_bf2(b.x * f, b.y * f),
+                            pack_bf2(b.z * f, b.w * f));
     }
 }
 
@@ -336,8 +390,8 @@ int dh_splits(int M, int D, int V, bool with_dW, int pairs)
 }
 
 struct LossPlan {
-    int rows, npieces, ntn, Vp, splits;
-    size_t stat, target, E, Hc, part, acc, bytes;   // workspace offsets
+    int rows, npieces, ntn, nst, Vp, splits;
+    size_t stat, target, wref, E, Hc, part, acc, bytes;   // workspace offsets
 };
 
 bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int rows)
@@ -347,6 +401,7 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
     L.rows = std::min(std::max(M, 1), grad ? (rows ? std::min(rows, kRowsMost) : kRowsDefault) : std::max(M, 1));
     L.npieces = M ? (M + L.rows - 1) / L.rows : 0;
     L.ntn = (V + kMmTile - 1) / kMmTile;
+    L.nst = (V + kMmHalf - 1) / kMmHalf;
     L.Vp = (V + 7) & ~7;
     size_t at = 0;
     auto take = [&](size_t b) {
@@ -354,8 +409,9 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
         at = up256(at + b);
         return o;
     };
-    L.stat = take((size_t)L.rows * L.ntn * sizeof(float2));
+    L.stat = take((size_t)L.rows * L.nst * sizeof(float2));
     L.target = take((size_t)L.rows * 4);
+    L.wref = take(grad ? 4 : 0);
     if (grad) {
         // the plan's pairs: those of the B200's 148 SMs, whatever the current device, so that the size is one number
         L.splits = dh_splits(L.rows, D, V, with_dW, 74);
@@ -378,6 +434,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     memset(&G, 0, sizeof(G));
     G.n = 1;
     mm_plan(G.p[0], M, V, D, true, 0, 1);
+    G.p[0].chunk = kChunk;
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.p[0].mA, true, false, H, M, D, D) || !mm_operand(&G.p[0].mB, true, false, W, V, D, D))
         return LB_ERR_INVALID_ARG;
@@ -388,7 +445,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
         E.target = (float *)(ws + L.target);
         E.M = M;
         E.V = V;
-        E.ntn = L.ntn;
+        E.nst = L.nst;
     };
     if (keep) {
         LogitEpi<true>::Params E;
@@ -411,6 +468,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     memset(&G, 0, sizeof(G));
     memset(&E, 0, sizeof(E));
     const void *Gm = ws + L.E;
+    E.wref = (const float *)(ws + L.wref);
     MmProb &P = G.p[0];
     mm_plan(P, M, D, V, true, 0, L.splits);
     P.b_mn = 1;
@@ -460,7 +518,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
         const size_t nvec = (size_t)M * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
         round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.part), (size_t)tile_rows * D / 4, P.splits, nvec,
-                                              (uint4 *)dH);
+                                              E.wref, (uint4 *)dH);
         ++*launches;
     }
     return status_from(cudaGetLastError());
@@ -506,7 +564,7 @@ extern "C" lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t 
     const lb_status st = logits(L, H, W, labels, M, D, V, ws, false, s);
     if (st != LB_OK) return st;
     lse_kernel<<<(M + 7) / 8, 256, 0, s>>>((const float2 *)(ws + L.stat), (const float *)(ws + L.target), labels, M, V,
-                                           L.ntn, loss, lse);
+                                           L.nst, loss, lse);
     set_launch_count(2);
     return status_from(cudaGetLastError());
 }
@@ -535,7 +593,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
         return LB_ERR_UNSUPPORTED;
     if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
     unsigned char *ws = (unsigned char *)workspace;
-    int launches = 0;
+    int launches = 1;
+    wref_kernel<<<1, 1024, 0, s>>>(weight, labels, M, V, (float *)(ws + L.wref));
     for (int p = 0; p < L.npieces; ++p) {
         const int r0 = p * L.rows, m = std::min(L.rows, M - r0);
         const uint16_t *Hp = H + (size_t)r0 * D;
@@ -543,7 +602,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
         if (st != LB_OK) return st;
         const dim3 grid((L.Vp + kGradCols - 1) / kGradCols, m);
         grad_kernel<<<grid, 256, 0, s>>>((uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
-                                         (const float *)(ws + L.target), labels + r0, weight + r0, V, L.Vp, L.ntn, D,
+                                         (const float *)(ws + L.target), labels + r0, weight + r0,
+                                         (const float *)(ws + L.wref), V, L.Vp, L.nst, D,
                                          (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0);
         launches += 2;
         st = products(L, W, m, D, V, dH + (size_t)r0 * D, dW, p == 0, ws, s, &launches);
@@ -552,7 +612,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     if (dW && L.npieces > 1) {
         const size_t nvec = (size_t)V * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
-        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.acc), 0, 1, nvec, (uint4 *)dW);
+        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.acc), 0, 1, nvec, (const float *)(ws + L.wref),
+                                              (uint4 *)dW);
         ++launches;
     }
     set_launch_count(launches);

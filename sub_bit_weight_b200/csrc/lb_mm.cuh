@@ -10,14 +10,22 @@
 // tile's i in its tensor memory and stages 128 i of A and 128 j of B per 64 k,
 // 32 KB for 128 x 256 x 64 multiply-adds.  A CTA by itself with the same
 // accumulator would have to stage 48 KB for them, and the operand stream from
-// L2 is what paces such a kernel.
+// L2 is what paces such a kernel.  A problem with few tiles takes them 128 or
+// 64 columns wide.
 //
-// Roles (6 warps a CTA): warp 0 one thread issues the TMA copies of its CTA's
+// Roles (12 warps a CTA): warp 0 one thread issues the TMA copies of its CTA's
 // halves; warp 1 of the pair's first CTA one thread issues the MMAs for both;
-// warps 2-5 the epilogue (128 rows of the CTA, one thread a row).  Two
-// accumulators of 256 columns let the epilogue of one unit overlap the main
-// loop of the next.  Units (tile, or a k range of a tile) are dealt to the
-// pairs in order; a launch may hold several problems.
+// warps 4-11 the epilogue (128 rows of the CTA, one thread a row and half of
+// the columns; an epilogue that holds its columns in registers takes registers
+// over from warps 0-3).  Two accumulators of 256 columns let the epilogue of one unit
+// overlap the main loop of the next.  Units (tile, or a k range of a tile) are
+// dealt to the pairs in order; a launch may hold several problems.
+//
+// The tensor core adds to its accumulator with truncation (measured: 16 terms
+// at a time, about 1.5 * 2^-24 of the accumulator lost on average, toward
+// zero), so a long sum of one sign comes out low by 9e-8 of its value per 16
+// terms, halved.  An epilogue can ask for `chunk` k blocks at a time and add
+// the chunks in registers, rounding to nearest.
 //
 // A problem is a batch of equal products, its operands arrays [z][row][column].
 // With parts = 3 each operand is a pair of halves (the planes z and z + 1: high
@@ -29,6 +37,8 @@
 // the kernel drains its copies and returns.
 #pragma once
 
+#include <algorithm>
+
 #include "lb_internal.cuh"
 #include "lb_tc.cuh"
 
@@ -38,7 +48,11 @@ constexpr int kMmTile = 256;      // i and j of a unit
 constexpr int kMmHalf = 128;      // i and j one CTA of the pair stages
 constexpr int kMmBK = 64;         // k of a stage
 constexpr int kMmStages = 6;
-constexpr int kMmThreads = 192;
+constexpr int kMmThreads = 384;
+constexpr int kMmEpiWarps = 8;
+// Registers a thread: 168 at launch (what 12 warps can have), then 56 and 2 x 224 by group of four warps, the same sum.
+constexpr int kMmRegsLaunch = 168, kMmRegsFew = 56, kMmRegsMany = 224;
+static_assert(kMmRegsFew + 2 * kMmRegsMany <= 3 * kMmRegsLaunch, "setmaxnreg.inc would wait for good");
 constexpr uint32_t kMmOperand = kMmHalf * kMmBK * 2;   // 16 KB: one operand's half of one stage
 constexpr uint32_t kMmSlice = kMmBK * 128;             // MN-major: 64 k rows of 64 elements
 
@@ -48,7 +62,7 @@ static __device__ int g_mm_err;
 struct MmSmem {
     alignas(1024) unsigned char A[kMmStages][kMmOperand];
     alignas(1024) unsigned char B[kMmStages][kMmOperand];
-    alignas(1024) unsigned char ST[4][32 * 128];   // one 32-row staging block per epilogue warp
+    alignas(1024) unsigned char ST[kMmEpiWarps][32 * 128];   // one 32-row staging block per epilogue warp
     uint64_t full[kMmStages], empty[kMmStages];
     uint64_t accf[2], acce[2];
     uint32_t tmem_base;
@@ -65,6 +79,8 @@ struct MmProb {
     int b_whole;          // with parts = 2: the low half taken is A's (else B's)
     int M, N;             // rows i, columns j
     int nkb;
+    int width;            // columns of a tile: 256, 128 or 64
+    int chunk;            // k blocks one accumulator takes
     int ntm, ntn, tiles;  // tiles across, along, and in all (fewer than across times along when symmetric)
     int m_fast;           // units run over i first (else over j first)
     int sym;
@@ -169,7 +185,7 @@ struct MmUnit {
     int q;             // problem
     int b;             // product of its batch
     int tm, tn, split;
-    int half;          // columns one CTA stages: half the tile's, 128 except in the last column of tiles
+    int half;          // columns one CTA stages: half the tile's, fewer in the last column of tiles
     int kb0, kb1;      // k blocks [kb0, kb1) of the concatenated segments
 };
 
@@ -219,8 +235,10 @@ __device__ __forceinline__ MmUnit mm_unit(const MmBatch<kMaxProbs> &G, int u)
     local -= r.b * P.tiles;
     if (P.sym) {
         r.tm = 0;
-        for (int left = P.ntn; local >= left; --left, ++r.tm) local -= left;   // row tm has ntn - tm tiles
-        r.tn = r.tm + local;
+        // tile row tm has the column tiles from its diagonal block on
+        const int per_row = kMmTile / P.width;
+        for (int left = P.ntn; local >= left; left -= per_row, ++r.tm) local -= left;
+        r.tn = r.tm * per_row + local;
     } else if (P.m_fast) {
         r.tn = local / P.ntm;
         r.tm = local - r.tn * P.ntm;
@@ -228,24 +246,24 @@ __device__ __forceinline__ MmUnit mm_unit(const MmBatch<kMaxProbs> &G, int u)
         r.tm = local / P.ntn;
         r.tn = local - r.tm * P.ntn;
     }
-    r.half = min(kMmHalf, ((P.N - r.tn * kMmTile + 31) & ~31) >> 1);
+    r.half = min(P.width, (P.N - r.tn * P.width + 31) & ~31) >> 1;
     const int total = P.nkb * P.parts;
     r.kb0 = r.split * P.kb_per;
     r.kb1 = min(total, r.kb0 + P.kb_per);
     return r;
 }
 
-// What an epilogue gets for one unit: the accumulator columns `tmem` of this warp's 32 rows (row = row0 + lane).
+// What an epilogue warp gets for one unit: 32 rows (row = row0 + lane) and `cols` columns from col0 on, which start at
+// tensor-memory address `tmem` (lane quarter in the upper half, column in the lower).  cols may be 0.
 struct MmTileCtx {
-    uint32_t tmem;        // tensor-memory address: lane quarter in the upper half, first column in the lower
-    int row0;             // first of this warp's 32 rows
-    int col0;             // first of the 256 columns
-    int lane;
+    uint32_t tmem;
+    int row0, col0, cols, lane;
     uint32_t st;          // this warp's 4 KB staging block (shared address)
 };
 
-// `Epi` has: struct Params; static __device__ void run(const Params &, const MmBatch &, const MmUnit &,
-// const MmTileCtx &, bool &stored); called by each epilogue warp once per unit.
+// An epilogue `Epi` is called by each of its warps, for each unit: begin() (before the accumulator is there), take() for
+// each chunk (`first`, `last`) while the accumulator is held, end() after it has been released.  `State` lives from
+// begin() to end(); kManyRegs asks for the register split; `stored` says whether the staging block has copies that may still be reading it.
 template <bool kBf16, int kMaxProbs, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     mm_kernel(const __grid_constant__ MmBatch<kMaxProbs> G, const __grid_constant__ typename Epi::Params E)
@@ -266,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&S.accf[b], 1);
-            mbar_init(&S.acce[b], 8);   // four epilogue warps of each CTA (the first CTA's barrier is the one used)
+            mbar_init(&S.acce[b], 2 * kMmEpiWarps);   // both CTAs' warps (the first CTA's barrier is the one used)
         }
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -281,115 +299,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
 
-    if (warp == 0) {
-        // ---------------- producer
-        if (lane == 0) {
-            uint32_t it = 0, pend = 0, pend_ph = 0;
-            for (int n = 0, u; (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
-                const MmUnit U = mm_unit(G, u);
-                const MmProb &P = G.p[U.q];
-                const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * kMmTile + (int)rank * U.half;
-                const bool two = !P.b_mn || U.half > 64;   // B's half needs both slices (a K-major box is whole)
-                const uint32_t bytes = 2 * (kMmOperand + (two ? kMmOperand : kMmSlice));   // both CTAs' halves
-                for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
-                    const int s = it % kMmStages;
-                    const uint32_t ph = (it / kMmStages) & 1;
-                    if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
-                    if (rank == 0) mbar_expect_tx(&S.full[s], bytes);
-                    const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
-                    // low halves first: the accumulator truncates, by what is already in it
-                    const int seg = kc / P.nkb, left = P.parts - 1 - seg;
-                    const int k = (kc - seg * P.nkb) * kMmBK;
-                    const int la = left == 2 || (left == 1 && P.b_whole), lb = left == 1 && !P.b_whole;
-                    const int za = U.b * P.za + (la ? 1 : 0), zb = U.b * P.zb + (lb ? 1 : 0);
-                    if (P.a_mn) {
-                        tma_load_3d_pair(S.A[s], &P.mA, i0, k, za, bar);
-                        tma_load_3d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k, za, bar);
-                    } else {
-                        tma_load_3d_pair(S.A[s], &P.mA, k, i0, za, bar);
-                    }
-                    if (P.b_mn) {
-                        tma_load_3d_pair(S.B[s], &P.mB, j0, k, zb, bar);
-                        if (two) tma_load_3d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k, zb, bar);
-                    } else {
-                        tma_load_3d_pair(S.B[s], &P.mB, k, j0, zb, bar);
-                    }
-                    pend |= 1u << s;
-                    pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
-                }
-            }
-            if (*abort) {
-                // let the copies already issued land before the pair leaves (bounded): the first CTA sees them on its
-                // barriers; the second, whose copies count there, waits a fixed time
-                const long long t0 = clock64();
-                if (rank == 0) {
-                    for (int s = 0; s < kMmStages; ++s)
-                        while ((pend >> s & 1) && !mbar_try_wait(&S.full[s], (pend_ph >> s) & 1) &&
-                               clock64() - t0 < kWaitCycles / 20) {
+    if (warp < 4) {
+        if constexpr (Epi::kManyRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kMmRegsFew));
+        if (warp == 0) {
+            // ---------------- producer
+            if (lane == 0) {
+                uint32_t it = 0, pend = 0, pend_ph = 0;
+                for (int n = 0, u; (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                    const MmUnit U = mm_unit(G, u);
+                    const MmProb &P = G.p[U.q];
+                    const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * P.width + (int)rank * U.half;
+                    const bool two = P.b_mn && U.half > 64;   // B's half needs both 64-column slices
+                    // both CTAs' halves; a K-major box has width / 2 rows
+                    const uint32_t bytes = 2 * (kMmOperand + (P.b_mn ? (two ? 2 : 1) * kMmSlice : P.width * kMmBK));
+                    for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
+                        const int s = it % kMmStages;
+                        const uint32_t ph = (it / kMmStages) & 1;
+                        if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
+                        if (rank == 0) mbar_expect_tx(&S.full[s], bytes);
+                        const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
+                        // low halves first: the accumulator truncates, by what is already in it
+                        const int seg = kc / P.nkb, left = P.parts - 1 - seg;
+                        const int k = (kc - seg * P.nkb) * kMmBK;
+                        const int la = left == 2 || (left == 1 && P.b_whole), lb = left == 1 && !P.b_whole;
+                        const int za = U.b * P.za + (la ? 1 : 0), zb = U.b * P.zb + (lb ? 1 : 0);
+                        if (P.a_mn) {
+                            tma_load_3d_pair(S.A[s], &P.mA, i0, k, za, bar);
+                            tma_load_3d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k, za, bar);
+                        } else {
+                            tma_load_3d_pair(S.A[s], &P.mA, k, i0, za, bar);
                         }
-                } else {
-                    while (clock64() - t0 < kWaitCycles / 1000) {
+                        if (P.b_mn) {
+                            tma_load_3d_pair(S.B[s], &P.mB, j0, k, zb, bar);
+                            if (two) tma_load_3d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k, zb, bar);
+                        } else {
+                            tma_load_3d_pair(S.B[s], &P.mB, k, j0, zb, bar);
+                        }
+                        pend |= 1u << s;
+                        pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
+                    }
+                }
+                if (*abort) {
+                    // let the copies already issued land before the pair leaves (bounded): the first CTA sees them on its
+                    // barriers; the second, whose copies count there, waits a fixed time
+                    const long long t0 = clock64();
+                    if (rank == 0) {
+                        for (int s = 0; s < kMmStages; ++s)
+                            while ((pend >> s & 1) && !mbar_try_wait(&S.full[s], (pend_ph >> s) & 1) &&
+                                   clock64() - t0 < kWaitCycles / 20) {
+                            }
+                    } else {
+                        while (clock64() - t0 < kWaitCycles / 1000) {
+                        }
                     }
                 }
             }
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer (first CTA of the pair)
-        if (lane == 0 && rank == 0) {
-            uint32_t it = 0, tcount = 0;
-            for (int u; (u = mm_nth(G, pair, npairs, (int)tcount)) >= 0 && !*abort; ++tcount) {
-                const MmUnit U = mm_unit(G, u);
-                const MmProb &P = G.p[U.q];
-                const int ab = tcount & 1;
-                const uint32_t aph = (tcount >> 1) & 1;
-                if (!mbar_wait(&S.acce[ab], aph ^ 1, abort, err, 2)) break;
-                tc_fence_after();
-                const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
-                const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn, 2 * U.half);
-                const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
-                // 16 k: 32 bytes along a K-major row, or two 8-row groups (2048 bytes) of an MN-major slice
-                const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (first CTA of the pair)
+            if (lane == 0 && rank == 0) {
+                uint32_t it = 0, acc = 0;   // stages, accumulators used
                 bool ok = true;
-                for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
-                    const int s = it % kMmStages;
-                    const uint32_t ph = (it / kMmStages) & 1;
-                    if (!mbar_wait(&S.full[s], ph, abort, err, 3)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t da = a_mn ? smem_desc_mn_sw128(S.A[s], kMmSlice) : smem_desc_sw128(S.A[s]);
-                    const uint64_t db = b_mn ? smem_desc_mn_sw128(S.B[s], kMmSlice) : smem_desc_sw128(S.B[s]);
+                for (int n = 0, u; ok && (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                    const MmUnit U = mm_unit(G, u);
+                    const MmProb &P = G.p[U.q];
+                    const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
+                    const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn, 2 * U.half);
+                    // 16 k: 32 bytes along a K-major row, or two 8-row groups (2048 bytes) of an MN-major slice
+                    const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
+                    for (int k0 = U.kb0; ok && k0 < U.kb1; k0 += P.chunk, ++acc) {
+                        const int ab = acc & 1, k1 = min(U.kb1, k0 + P.chunk);
+                        if (!(ok = mbar_wait(&S.acce[ab], ((acc >> 1) & 1) ^ 1, abort, err, 2))) break;
+                        tc_fence_after();
+                        const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
+                        for (int kc = k0; kc < k1; ++kc, ++it) {
+                            const int s = it % kMmStages;
+                            const uint32_t ph = (it / kMmStages) & 1;
+                            if (!(ok = mbar_wait(&S.full[s], ph, abort, err, 3))) break;
+                            tc_fence_after();
+                            const uint64_t da = a_mn ? smem_desc_mn_sw128(S.A[s], kMmSlice) : smem_desc_sw128(S.A[s]);
+                            const uint64_t db = b_mn ? smem_desc_mn_sw128(S.B[s], kMmSlice) : smem_desc_sw128(S.B[s]);
 #pragma unroll
-                    for (int kk = 0; kk < kMmBK / 16; ++kk)
-                        tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, (kc > U.kb0 || kk) ? 1u : 0u);
-                    tc_commit_pair(&S.empty[s]);
+                            for (int kk = 0; kk < kMmBK / 16; ++kk)
+                                tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, (kc > k0 || kk) ? 1u : 0u);
+                            tc_commit_pair(&S.empty[s]);
+                        }
+                        if (ok) tc_commit_pair(&S.accf[ab]);
+                    }
                 }
-                if (!ok) break;
-                tc_commit_pair(&S.accf[ab]);
             }
         }
     } else {
-        // ---------------- epilogue (warps 2-5: tensor-memory lanes 32 (warp % 4) ..)
-        const int q4 = warp & 3;
-        uint32_t tcount = 0;
-        bool stored = false;
+        if constexpr (Epi::kManyRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kMmRegsMany));
+        // ---------------- epilogue (warps 4-11: tensor-memory lanes 32 (warp % 4) .., one half of the columns)
+        const int q4 = warp & 3, side = (warp - 4) >> 2;
+        uint32_t acc = 0;
+        bool stored = false, ok = true;
         MmTileCtx T;
         T.lane = lane;
-        T.st = smem_u32(S.ST[q4]);
-        for (int u; (u = mm_nth(G, pair, npairs, (int)tcount)) >= 0 && !*abort; ++tcount) {
+        T.st = smem_u32(S.ST[warp - 4]);
+        for (int n = 0, u; ok && (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
             const MmUnit U = mm_unit(G, u);
-            const int ab = tcount & 1;
-            const uint32_t aph = (tcount >> 1) & 1;
-            if (!mbar_wait(&S.accf[ab], aph, abort, err, 4)) break;
-            tc_fence_after();
-            T.tmem = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(ab * kMmTile);
+            const MmProb &P = G.p[U.q];
             T.row0 = U.tm * kMmTile + (int)rank * kMmHalf + q4 * 32;
-            T.col0 = U.tn * kMmTile;
-            Epi::run(E, G, U, T, stored);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acce[ab]), 0));
+            T.col0 = U.tn * P.width + side * (P.width / 2);
+            T.cols = T.row0 < P.M ? max(0, min(P.width / 2, P.N - T.col0)) : 0;
+            typename Epi::State state;
+            Epi::begin(E, P, U, T, state);
+            for (int k0 = U.kb0; k0 < U.kb1; k0 += P.chunk, ++acc) {
+                const int ab = acc & 1;
+                if (!(ok = mbar_wait(&S.accf[ab], (acc >> 1) & 1, abort, err, 4))) break;
+                tc_fence_after();
+                T.tmem = tmem + ((uint32_t)(q4 * 32) << 16) + (uint32_t)(ab * kMmTile + side * (P.width / 2));
+                Epi::take(E, P, U, T, state, k0 == U.kb0, k0 + P.chunk >= U.kb1, stored);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.acce[ab]), 0));
+            }
+            if (ok) Epi::end(E, P, U, T, state, stored);
         }
         if (lane == 0) tma_store_wait_all();
     }
@@ -404,18 +430,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 }
 
 // Host: an operand stored as `planes` planes of `rows` rows of `cols` elements, `pitch` elements between rows and
-// `plane` between planes.  K-major: a row is an i (or j) and the box is 64 k x 128 rows; MN-major: a row is a k and the
-// box is 64 i x 64 k rows.  Everything outside reads as zero.
+// `plane` between planes.  K-major: a row is an i (or j) and the box is 64 k x `box` rows (128 for A, half a tile's
+// columns for B); MN-major: a row is a k and the box is 64 i x 64 k rows.  Everything outside reads as zero.
 inline bool mm_operand(CUtensorMap *map, bool bf16, bool mn_major, const void *base, long rows, long cols, long pitch,
-                       long planes = 1, long plane = 0)
+                       long planes = 1, int box = kMmHalf, long plane = 0)
 {
     return tmap_encode_3d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols,
-                          rows, planes, pitch * 2, (plane ? plane : pitch * rows) * 2, 64, mn_major ? kMmBK : kMmHalf);
+                          rows, planes, pitch * 2, (plane ? plane : pitch * rows) * 2, 64, mn_major ? kMmBK : box);
+}
+
+inline int mm_tiles(int ntm, int ntn, bool sym, int width)
+{
+    if (!sym) return ntm * ntn;
+    int t = 0;
+    for (int i = 0; i < ntm; ++i) t += std::max(0, ntn - i * (kMmTile / width));
+    return t;
 }
 
 // Host: tiles and k ranges of a problem whose k blocks are cut into (at most) `splits` ranges.
 inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int splits, int parts = 1, int batch = 1,
-                    bool sym = false)
+                    bool sym = false, int width = kMmTile)
 {
     P.M = M;
     P.N = N;
@@ -424,8 +458,10 @@ inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int
     P.sym = sym ? 1 : 0;
     P.nkb = (int)((K + kMmBK - 1) / kMmBK);
     P.ntm = (M + kMmTile - 1) / kMmTile;
-    P.ntn = (N + kMmTile - 1) / kMmTile;
-    P.tiles = sym ? P.ntn * (P.ntn + 1) / 2 : P.ntm * P.ntn;
+    P.width = width;
+    P.ntn = (N + width - 1) / width;
+    P.tiles = mm_tiles(P.ntm, P.ntn, sym, width);
+    P.chunk = 1 << 28;
     P.m_fast = m_fast ? 1 : 0;
     P.unit0 = unit0;
     const int total = P.nkb * parts;
@@ -449,6 +485,14 @@ inline cudaError_t mm_launch(const MmBatch<kMaxProbs> &G, const typename Epi::Pa
     const void *fn = (const void *)mm_kernel<kBf16, kMaxProbs, Epi>;
     cudaError_t e = ensure_dyn_smem(fn, kMmSmemBytes);
     if (e != cudaSuccess) return e;
+    if (Epi::kManyRegs) {
+        // the register split counts on this: with fewer at launch, setmaxnreg would wait for registers that do not exist
+        static const int regs = [fn]() {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, fn) == cudaSuccess ? a.numRegs : 0;
+        }();
+        if (regs < kMmRegsLaunch) return cudaErrorInvalidConfiguration;
+    }
     int pairs = 0;
     if ((e = mm_pairs(&pairs)) != cudaSuccess) return e;
     if (pairs > G.nunits) pairs = G.nunits;

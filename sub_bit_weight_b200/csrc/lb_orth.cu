@@ -181,22 +181,45 @@ struct OrthProb {
     int ldo;              // kOut: columns of the output
 };
 struct OrthEpi {
+    static constexpr bool kManyRegs = true;
     struct Params {
         OrthProb p[kMostProbs];
         uint16_t *out[kMostMats];
         const float2 *scal;
     };
-    static __device__ __forceinline__ void run(const Params &E, const MmBatch<kMostProbs> &G, const MmUnit &U,
-                                               const MmTileCtx &T, bool &stored)
+    struct State {
+        uint4 hi[4], lo[4];   // kSym: the first 32 elements of C
+    };
+    static __device__ __forceinline__ void load_c(const OrthProb &O, const MmProb &P, const MmUnit &U, int row, int col,
+                                                  uint4 (&hi)[4], uint4 (&lo)[4])
     {
-        const MmProb &P = G.p[U.q];
-        if (T.row0 >= P.M) return;
+        const size_t plane = (size_t)P.N * O.pn;
+        const __half *C = O.C + (size_t)U.b * 2 * plane + (size_t)row * O.pn + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = row < P.M && col + 8 * i < O.pn && col + 31 >= row;
+            hi[i] = in ? *reinterpret_cast<const uint4 *>(C + 8 * i) : make_uint4(0, 0, 0, 0);
+            lo[i] = in ? *reinterpret_cast<const uint4 *>(C + plane + 8 * i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void begin(const Params &E, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
+                                                 State &S)
+    {
+        if (E.p[U.q].kind == kSym && T.cols > 0) load_c(E.p[U.q], P, U, T.row0 + T.lane, T.col0, S.hi, S.lo);
+    }
+    static __device__ __forceinline__ void end(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &,
+                                               bool &)
+    {
+    }
+    static __device__ __forceinline__ void take(const Params &E, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
+                                                State &S, bool, bool, bool &stored)
+    {
         const OrthProb &O = E.p[U.q];
-        const int row = T.row0 + T.lane, cols = min(kMmTile, P.N - T.col0);
+        const int row = T.row0 + T.lane;
         uint32_t v[32];
         if (O.kind == kPart) {
             const int z = U.split * P.batch + U.b;
-            for (int c = 0; c < cols; c += 32) {
+            for (int c = 0; c < T.cols; c += 32) {
                 tmem_ld32(T.tmem + c, v);
                 if (stored) {
                     if (T.lane == 0) tma_store_wait_read();
@@ -213,13 +236,12 @@ struct OrthEpi {
             return;
         }
         if (O.kind == kOut) {
+            if (T.cols == 0) return;
             uint16_t *const base = E.out[O.first + U.b];
-            uint16_t *dst = base + (size_t)row * O.ldo + T.col0;
             const float f = O.alpha * E.scal[O.first + U.b].x;
             const bool vec = O.ldo % 8 == 0 && ((uintptr_t)base & 15) == 0;
-            for (int c = 0; c < cols; c += 32) {
+            for (int c = 0; c < T.cols; c += 32) {
                 tmem_ld32(T.tmem + c, v);
-                if (row >= P.M) continue;
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -227,45 +249,52 @@ struct OrthEpi {
                         : "=r"(w[i])
                         : "f"(__uint_as_float(v[2 * i + 1]) * f), "f"(__uint_as_float(v[2 * i]) * f));
                 if (vec) {
+                    uint16_t *dst = base + (size_t)row * O.ldo + T.col0 + c;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (c + 8 * i < cols)
-                            *reinterpret_cast<uint4 *>(dst + c + 8 * i) =
+                        if (row < P.M && c + 8 * i < T.cols)
+                            *reinterpret_cast<uint4 *>(dst + 8 * i) =
                                 make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 } else {
+                    // rows without alignment: through the staging block (32 rows of 32, 66 bytes apart), then one row
+                    // of 32 columns at a time
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (c + i < cols) dst[c + i] = (uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+                        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)(T.lane * 66 + 2 * i)),
+                                     "h"((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]))
+                                     : "memory");
+                    __syncwarp();
+                    const int rows = min(32, P.M - T.row0);
+                    uint16_t *dst = base + (size_t)T.row0 * O.ldo + T.col0 + c + T.lane;
+                    if (c + T.lane < T.cols)
+                        for (int r = 0; r < rows; ++r) {
+                            uint16_t y;
+                            asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(y) : "r"(T.st + (uint32_t)(r * 66 + 2 * T.lane)));
+                            dst[(size_t)r * O.ldo] = y;
+                        }
                 }
             }
             return;
         }
         // A symmetric n x n matrix: every element on or above the diagonal is computed once and written to both its
         // places.  (The products of a polynomial's factors are symmetric only up to rounding, and a difference between
-        // the triangles would grow by q(0)^2 = 12 a step, twice as fast in its exponent as the matrix itself.)
+        // the triangles would grow by q(0)^2 = 12 a step.)
         const size_t plane = (size_t)P.N * O.pn;
-        const __half *C = O.C + (size_t)U.b * 2 * plane;
-        for (int c = 0; c < cols; c += 32) {
+        for (int c = 0; c < T.cols; c += 32) {
             tmem_ld32(T.tmem + c, v);
             const int col0 = T.col0 + c;
-            if (row >= P.M || col0 + 31 < row) continue;
             float x[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                alignas(16) __half ch[8], cl[8];
-                const bool in = col0 + 8 * i < O.pn;
-                if (in) {
-                    *reinterpret_cast<uint4 *>(ch) =
-                        *reinterpret_cast<const uint4 *>(C + (size_t)row * O.pn + col0 + 8 * i);
-                    *reinterpret_cast<uint4 *>(cl) =
-                        *reinterpret_cast<const uint4 *>(C + plane + (size_t)row * O.pn + col0 + 8 * i);
-                }
+                const __half *ch = reinterpret_cast<const __half *>(&S.hi[i]), *cl = reinterpret_cast<const __half *>(&S.lo[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float y = in ? __half2float(ch[j]) + __half2float(cl[j]) : 0.0f;
-                    x[8 * i + j] = fmaf(__uint_as_float(v[8 * i + j]), O.alpha, O.beta * y);
-                }
+                for (int j = 0; j < 8; ++j)
+                    x[8 * i + j] = fmaf(__uint_as_float(v[8 * i + j]), O.alpha,
+                                        O.beta * (__half2float(ch[j]) + __half2float(cl[j])));
             }
+            if (c + 32 < T.cols) load_c(O, P, U, row, col0 + 32, S.hi, S.lo);
+            if (row >= P.M || col0 + 31 < row) continue;
             put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, row, col0, P.N);
             if (O.D2) {
 #pragma unroll
@@ -613,6 +642,30 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     E.scal = M.scal;
     for (int i = 0; i < M.n; ++i) E.out[i] = Os[C.order[i]];
     const int parts = bf16 ? 1 : 3, xz = bf16 ? 1 : 2;
+    int pairs = 0;
+    cudaError_t e = mm_pairs(&pairs);
+    if (e != cudaSuccess) return status_from(e);
+    // Widest tiles of a launch that still give every pair of SMs one: a few small matrices are bound by the length of one
+    // tile's chain (copy, products, epilogue), many or large ones by the operands read per tile.
+    auto width_of = [&](auto &&tiles) {
+        int w = kMmTile;
+        while (w > 64 && tiles(w) < pairs) w >>= 1;
+        return w;
+    };
+    auto square_tiles = [&](int w) {
+        long t = 0;
+        for (const Group &g : C.groups)
+            if (g.n > kSmallN)
+                t += (long)g.batch * mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + w - 1) / w, true, w);
+        return t;
+    };
+    auto update_tiles = [&](int w) {
+        long t = 0;
+        for (const Group &g : C.groups)
+            t += (long)g.batch * ((g.rows + kMmTile - 1) / kMmTile) * ((g.cols + w - 1) / w);
+        return t;
+    };
+    const int wq = width_of(square_tiles), wo = width_of(update_tiles);
     bool ok = true;
     auto begin = [&]() { memset(&B, 0, sizeof(B)); };
     auto launch = [&]() -> cudaError_t {
@@ -620,7 +673,6 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         ++*launches;
         return mm_launch<false, kMostProbs, OrthEpi>(B, E, s);
     };
-    cudaError_t e;
 
     // A_0: both operands are X, contracted over the long axis
     begin();
@@ -679,10 +731,10 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     auto square = [&](const Group &g, size_t x, size_t y, size_t d, float alpha, float beta, size_t c) -> OrthProb & {
         MmProb &P = B.p[B.n];
         OrthProb &O = E.p[B.n];
-        mm_plan(P, g.n, g.n, g.n, false, B.nunits, 1, 3, g.batch, true);
+        mm_plan(P, g.n, g.n, g.n, false, B.nunits, 1, 3, g.batch, true, wq);
         P.za = P.zb = 2;
         ok = ok && mm_operand(&P.mA, false, false, ws + x, g.n, g.n, g.pn, 2L * g.batch) &&
-             mm_operand(&P.mB, false, false, ws + y, g.n, g.n, g.pn, 2L * g.batch);
+             mm_operand(&P.mB, false, false, ws + y, g.n, g.n, g.pn, 2L * g.batch, wq / 2);
         O.kind = kSym;
         O.pn = g.pn;
         O.first = g.first;
@@ -735,9 +787,9 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         OrthProb &O = E.p[B.n];
         const bool sm = g.n <= kSmallN;
         const size_t Q = sm ? g.A : (steps - 1) & 1 ? g.Q1 : g.Q0;
-        mm_plan(P, g.rows, g.cols, g.n, false, B.nunits, 1, bf16 ? 2 : 3, g.batch);
+        mm_plan(P, g.rows, g.cols, g.n, false, B.nunits, 1, bf16 ? 2 : 3, g.batch, false, wo);
         CUtensorMap mQ, mX;
-        ok = ok && mm_operand(&mQ, false, false, ws + Q, g.n, g.n, g.pn, 2L * g.batch) &&
+        ok = ok && mm_operand(&mQ, false, false, ws + Q, g.n, g.n, g.pn, 2L * g.batch, g.wide ? kMmHalf : wo / 2) &&
              mm_operand(&mX, false, g.wide, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
         P.mA = g.wide ? mQ : mX;
         P.mB = g.wide ? mX : mQ;
