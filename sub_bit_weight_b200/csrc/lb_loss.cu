@@ -436,7 +436,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     mm_plan(G.p[0], M, V, D, true, 0, 1);
     G.p[0].chunk = kChunk;
     G.nunits = mm_units(G.p[0]);
-    if (!mm_operand(&G.p[0].mA, true, false, H, M, D, D) || !mm_operand(&G.p[0].mB, true, false, W, V, D, D))
+    if (!mm_operand(&G.mA[0], true, false, H, M, D, D) || !mm_operand(&G.mB[0], true, false, W, V, D, D))
         return LB_ERR_INVALID_ARG;
     auto fill = [&](auto &E) {
         memset(&E, 0, sizeof(E));
@@ -472,7 +472,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     MmProb &P = G.p[0];
     mm_plan(P, M, D, V, true, 0, L.splits);
     P.b_mn = 1;
-    if (!mm_operand(&P.mA, true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&P.mB, true, true, W, V, D, D))
+    if (!mm_operand(&G.mA[0], true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[0], true, true, W, V, D, D))
         return LB_ERR_INVALID_ARG;
     const int tile_rows = P.ntm * kMmTile;
     bool ok;
@@ -492,7 +492,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
         MmProb &Q = G.p[1];
         mm_plan(Q, V, D, M, false, G.nunits, 1);
         Q.a_mn = Q.b_mn = 1;
-        if (!mm_operand(&Q.mA, true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&Q.mB, true, true, ws + L.Hc, M, D, D))
+        if (!mm_operand(&G.mA[1], true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[1], true, true, ws + L.Hc, M, D, D))
             return LB_ERR_INVALID_ARG;
         if (L.npieces > 1) {
             E.kind[1] = first ? kOutF32 : kOutF32Add;

@@ -13,8 +13,8 @@
 // L2 is what paces such a kernel.  A problem with few tiles takes them 128 or
 // 64 columns wide.
 //
-// Roles (12 warps a CTA): warp 0 one thread issues the TMA copies of its CTA's
-// halves; warp 1 of the pair's first CTA one thread issues the MMAs for both;
+// Roles (12 warps a CTA): one thread each of warps 0 and 2 issues the TMA
+// copies of its CTA's half of A and of B; warp 1 of the pair's first CTA one thread issues the MMAs for both;
 // warps 4-11 the epilogue (128 rows of the CTA, one thread a row and half of
 // the columns; an epilogue that holds its columns in registers takes registers
 // over from warps 0-3).  Two accumulators of 256 columns let the epilogue of one unit
@@ -54,26 +54,15 @@ constexpr int kMmEpiWarps = 8;
 constexpr int kMmRegsLaunch = 168, kMmRegsFew = 56, kMmRegsMany = 224;
 static_assert(kMmRegsFew + 2 * kMmRegsMany <= 3 * kMmRegsLaunch, "setmaxnreg.inc would wait for good");
 constexpr uint32_t kMmOperand = kMmHalf * kMmBK * 2;   // 16 KB: one operand's half of one stage
+constexpr int kMmChunkAll = 1 << 28;
 constexpr uint32_t kMmSlice = kMmBK * 128;             // MN-major: 64 k rows of 64 elements
 
 // Error code of a bounded wait that gave up, one per source file that has such kernels (mm_status).
 static __device__ int g_mm_err;
 
-struct MmSmem {
-    alignas(1024) unsigned char A[kMmStages][kMmOperand];
-    alignas(1024) unsigned char B[kMmStages][kMmOperand];
-    alignas(1024) unsigned char ST[kMmEpiWarps][32 * 128];   // one 32-row staging block per epilogue warp
-    uint64_t full[kMmStages], empty[kMmStages];
-    uint64_t accf[2], acce[2];
-    uint32_t tmem_base;
-    int abort;
-};
-constexpr size_t kMmSmemBytes = sizeof(MmSmem) + 1024;
-
 // One problem of a launch: `batch` products of M x N over nkb 64-deep k blocks, three times as many with parts = 3.
 // a_mn / b_mn: the operand is MN-major.  za, zb: its z planes from one product of the batch to the next.
 struct MmProb {
-    CUtensorMap mA, mB;
     int a_mn, b_mn;
     int parts, za, zb;
     int b_whole;          // with parts = 2: the low half taken is A's (else B's)
@@ -87,6 +76,20 @@ struct MmProb {
     int batch, splits, kb_per;   // k blocks are cut into `splits` ranges of kb_per
     int unit0;            // first unit of this problem
 };
+
+template <int kMaxProbs>
+struct MmSmem {
+    alignas(1024) unsigned char A[kMmStages][kMmOperand];
+    alignas(1024) unsigned char B[kMmStages][kMmOperand];
+    alignas(1024) unsigned char ST[kMmEpiWarps][32 * 128];   // one 32-row staging block per epilogue warp
+    uint64_t full[kMmStages], empty[kMmStages];
+    uint64_t accf[2], acce[2];
+    MmProb p[kMaxProbs];   // the launch's records: parameters are read from far away, one latency after another
+    uint32_t tmem_base;
+    int abort;
+};
+template <int kMaxProbs>
+constexpr size_t kMmSmemBytes = sizeof(MmSmem<kMaxProbs>) + 1024;
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -191,6 +194,7 @@ struct MmUnit {
 
 template <int kMaxProbs>
 struct MmBatch {
+    CUtensorMap mA[kMaxProbs], mB[kMaxProbs];
     MmProb p[kMaxProbs];
     int n, nunits;
     int extra;            // see mm_nth
@@ -199,13 +203,13 @@ struct MmBatch {
 // The k-th unit of a pair, -1 after its last.  Units are dealt in order, except that where a first problem of long units
 // leaves some pairs one short, those pairs first take `extra` units each of what follows, which fills the gap.
 template <int kMaxProbs>
-__device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, int pair, int npairs, int k)
+__device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, const MmProb *p, int pair, int npairs, int k)
 {
     if (G.extra == 0) {
         const int u = pair + k * npairs;
         return u < G.nunits ? u : -1;
     }
-    const int n0 = G.p[1].unit0, more = n0 % npairs;   // pairs below `more` have one long unit more
+    const int n0 = p[1].unit0, more = n0 % npairs;   // pairs below `more` have one long unit more
     const int c0 = n0 / npairs + (pair < more ? 1 : 0);
     if (k < c0) return pair + k * npairs;
     k -= c0;
@@ -218,14 +222,13 @@ __device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, int pair, int
     return u < G.nunits ? u : -1;
 }
 
-template <int kMaxProbs>
-__device__ __forceinline__ MmUnit mm_unit(const MmBatch<kMaxProbs> &G, int u)
+__device__ __forceinline__ MmUnit mm_unit(const MmProb *p, int nprobs, int u)
 {
     MmUnit r;
     r.q = 0;
-    for (int i = 1; i < G.n; ++i)
-        if (u >= G.p[i].unit0) r.q = i;
-    const MmProb &P = G.p[r.q];
+    for (int i = 1; i < nprobs; ++i)
+        if (u >= p[i].unit0) r.q = i;
+    const MmProb &P = p[r.q];
     // ranges of k outermost: the units in flight share operands
     int local = u - P.unit0;
     const int per_range = P.tiles * P.batch;
@@ -271,12 +274,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     int *const err = &g_mm_err;
     extern __shared__ __align__(1024) unsigned char mm_raw[];
     const uint32_t raw_addr = smem_u32(mm_raw);
-    MmSmem &S = *reinterpret_cast<MmSmem *>(mm_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
+    MmSmem<kMaxProbs> &S = *reinterpret_cast<MmSmem<kMaxProbs> *>(mm_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     volatile int *abort = &S.abort;
+    const int nprobs = G.n;
 
+    for (int i = threadIdx.x; i < nprobs * (int)(sizeof(MmProb) / 4); i += kMmThreads)
+        reinterpret_cast<int *>(S.p)[i] = reinterpret_cast<const int *>(G.p)[i];
+    if (warp == 3 && lane < nprobs) {
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&G.mA[lane]) : "memory");
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&G.mB[lane]) : "memory");
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMmStages; ++s) {
             mbar_init(&S.full[s], 1);
@@ -298,90 +308,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
+    // Launched to overlap with the kernel before it (see mm_launch): what follows reads and writes memory that kernel
+    // may still be using, so wait for it to finish; the next kernel may come up as soon as this one has got here.
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
     if (warp < 4) {
         if constexpr (Epi::kManyRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kMmRegsFew));
-        if (warp == 0) {
-            // ---------------- producer
+        // What the loops below use of a problem is in registers before they start: one of these threads has about 500
+        // cycles for a k block, and a shared-memory read is 30 of them.
+        if (warp == 0 || warp == 2) {
+            // ---------------- producers: warp 0 copies A, warp 2 B
             if (lane == 0) {
-                uint32_t it = 0, pend = 0, pend_ph = 0;
-                for (int n = 0, u; (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
-                    const MmUnit U = mm_unit(G, u);
-                    const MmProb &P = G.p[U.q];
-                    const int i0 = U.tm * kMmTile + (int)rank * kMmHalf, j0 = U.tn * P.width + (int)rank * U.half;
-                    const bool two = P.b_mn && U.half > 64;   // B's half needs both 64-column slices
-                    // both CTAs' halves; a K-major box has width / 2 rows
-                    const uint32_t bytes = 2 * (kMmOperand + (P.b_mn ? (two ? 2 : 1) * kMmSlice : P.width * kMmBK));
-                    for (int kc = U.kb0; kc < U.kb1; ++kc, ++it) {
-                        const int s = it % kMmStages;
-                        const uint32_t ph = (it / kMmStages) & 1;
-                        if (!mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1)) break;
-                        if (rank == 0) mbar_expect_tx(&S.full[s], bytes);
-                        const uint32_t bar = map_rank(smem_u32(&S.full[s]), 0);
-                        // low halves first: the accumulator truncates, by what is already in it
-                        const int seg = kc / P.nkb, left = P.parts - 1 - seg;
-                        const int k = (kc - seg * P.nkb) * kMmBK;
-                        const int la = left == 2 || (left == 1 && P.b_whole), lb = left == 1 && !P.b_whole;
-                        const int za = U.b * P.za + (la ? 1 : 0), zb = U.b * P.zb + (lb ? 1 : 0);
-                        if (P.a_mn) {
-                            tma_load_3d_pair(S.A[s], &P.mA, i0, k, za, bar);
-                            tma_load_3d_pair(S.A[s] + kMmSlice, &P.mA, i0 + 64, k, za, bar);
+                const bool is_a = warp == 0;
+                unsigned char *const base = is_a ? S.A[0] : S.B[0];
+                const uint32_t full0 = map_rank(smem_u32(&S.full[0]), 0);
+                uint32_t s = 0, ph = 0;
+                bool ok = true;
+                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                    const MmUnit U = mm_unit(S.p, nprobs, u);
+                    const MmProb &P = S.p[U.q];
+                    const CUtensorMap *const map = is_a ? &G.mA[U.q] : &G.mB[U.q];
+                    const bool mn = is_a ? P.a_mn != 0 : P.b_mn != 0;
+                    const bool two = mn && (is_a || U.half > 64);   // both 64-wide slices
+                    const int x0 = is_a ? U.tm * kMmTile + (int)rank * kMmHalf : U.tn * P.width + (int)rank * U.half;
+                    // both CTAs' halves of both operands; a K-major box of B has width / 2 rows
+                    const uint32_t bytes =
+                        2 * (kMmOperand + (P.b_mn ? (U.half > 64 ? 2 : 1) * kMmSlice : P.width * kMmBK));
+                    const int nkb = P.nkb, parts = P.parts, z0 = U.b * (is_a ? P.za : P.zb);
+                    // low halves first (the accumulator truncates by what is already in it): with three parts
+                    // lo * hi, hi * lo, hi * hi; with two the operand that has a low half
+                    const int low = parts == 3 ? (is_a ? 0 : 1) : parts == 2 && (is_a == (P.b_whole != 0)) ? 0 : -1;
+                    int seg = U.kb0 / nkb, kb = U.kb0 - seg * nkb;
+                    for (int left = U.kb1 - U.kb0; left > 0; --left) {
+                        if (!(ok = mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1))) break;
+                        if (is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
+                        unsigned char *const dst = base + s * kMmOperand;
+                        const uint32_t bar = full0 + s * 8;
+                        const int k = kb * kMmBK, z = z0 + (seg == low ? 1 : 0);
+                        if (mn) {
+                            tma_load_3d_pair(dst, map, x0, k, z, bar);
+                            if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z, bar);
                         } else {
-                            tma_load_3d_pair(S.A[s], &P.mA, k, i0, za, bar);
+                            tma_load_3d_pair(dst, map, k, x0, z, bar);
                         }
-                        if (P.b_mn) {
-                            tma_load_3d_pair(S.B[s], &P.mB, j0, k, zb, bar);
-                            if (two) tma_load_3d_pair(S.B[s] + kMmSlice, &P.mB, j0 + 64, k, zb, bar);
-                        } else {
-                            tma_load_3d_pair(S.B[s], &P.mB, k, j0, zb, bar);
+                        if (++kb == nkb) {
+                            kb = 0;
+                            ++seg;
                         }
-                        pend |= 1u << s;
-                        pend_ph = (pend_ph & ~(1u << s)) | (ph << s);
+                        if (++s == kMmStages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
                 }
                 if (*abort) {
-                    // let the copies already issued land before the pair leaves (bounded): the first CTA sees them on its
-                    // barriers; the second, whose copies count there, waits a fixed time
+                    // let the copies already issued land before the pair leaves: a wait gives up after two seconds, a copy
+                    // takes microseconds, so a fixed time is enough
                     const long long t0 = clock64();
-                    if (rank == 0) {
-                        for (int s = 0; s < kMmStages; ++s)
-                            while ((pend >> s & 1) && !mbar_try_wait(&S.full[s], (pend_ph >> s) & 1) &&
-                                   clock64() - t0 < kWaitCycles / 20) {
-                            }
-                    } else {
-                        while (clock64() - t0 < kWaitCycles / 1000) {
-                        }
+                    while (clock64() - t0 < kWaitCycles / 1000) {
                     }
                 }
             }
         } else if (warp == 1) {
             // ---------------- MMA issuer (first CTA of the pair)
             if (lane == 0 && rank == 0) {
-                uint32_t it = 0, acc = 0;   // stages, accumulators used
+                uint32_t s = 0, ph = 0, acc = 0;   // stage, its phase, accumulators used
                 bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
-                    const MmUnit U = mm_unit(G, u);
-                    const MmProb &P = G.p[U.q];
+                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                    const MmUnit U = mm_unit(S.p, nprobs, u);
+                    const MmProb &P = S.p[U.q];
                     const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
                     const uint32_t idesc = mm_idesc(kBf16, a_mn, b_mn, 2 * U.half);
                     // 16 k: 32 bytes along a K-major row, or two 8-row groups (2048 bytes) of an MN-major slice
                     const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
-                    for (int k0 = U.kb0; ok && k0 < U.kb1; k0 += P.chunk, ++acc) {
-                        const int ab = acc & 1, k1 = min(U.kb1, k0 + P.chunk);
+                    const uint64_t da0 = a_mn ? smem_desc_mn_sw128(S.A[0], kMmSlice) : smem_desc_sw128(S.A[0]);
+                    const uint64_t db0 = b_mn ? smem_desc_mn_sw128(S.B[0], kMmSlice) : smem_desc_sw128(S.B[0]);
+                    const int chunk = P.chunk;
+                    for (int left = U.kb1 - U.kb0; ok && left > 0; left -= chunk, ++acc) {
+                        const int ab = acc & 1;
                         if (!(ok = mbar_wait(&S.acce[ab], ((acc >> 1) & 1) ^ 1, abort, err, 2))) break;
                         tc_fence_after();
                         const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
-                        for (int kc = k0; kc < k1; ++kc, ++it) {
-                            const int s = it % kMmStages;
-                            const uint32_t ph = (it / kMmStages) & 1;
+                        uint32_t add = 0;
+                        for (int i = min(left, chunk); i > 0; --i) {
                             if (!(ok = mbar_wait(&S.full[s], ph, abort, err, 3))) break;
                             tc_fence_after();
-                            const uint64_t da = a_mn ? smem_desc_mn_sw128(S.A[s], kMmSlice) : smem_desc_sw128(S.A[s]);
-                            const uint64_t db = b_mn ? smem_desc_mn_sw128(S.B[s], kMmSlice) : smem_desc_sw128(S.B[s]);
+                            const uint64_t da = da0 + s * (kMmOperand >> 4), db = db0 + s * (kMmOperand >> 4);
+                            tc_mma_f16_pair(dacc, da, db, idesc, add);
 #pragma unroll
-                            for (int kk = 0; kk < kMmBK / 16; ++kk)
-                                tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, (kc > k0 || kk) ? 1u : 0u);
+                            for (int kk = 1; kk < kMmBK / 16; ++kk)
+                                tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, 1u);
                             tc_commit_pair(&S.empty[s]);
+                            add = 1;
+                            if (++s == kMmStages) {
+                                s = 0;
+                                ph ^= 1;
+                            }
                         }
                         if (ok) tc_commit_pair(&S.accf[ab]);
                     }
@@ -397,9 +420,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         MmTileCtx T;
         T.lane = lane;
         T.st = smem_u32(S.ST[warp - 4]);
-        for (int n = 0, u; ok && (u = mm_nth(G, pair, npairs, n)) >= 0 && !*abort; ++n) {
-            const MmUnit U = mm_unit(G, u);
-            const MmProb &P = G.p[U.q];
+        for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+            const MmUnit U = mm_unit(S.p, nprobs, u);
+            const MmProb &P = S.p[U.q];
             T.row0 = U.tm * kMmTile + (int)rank * kMmHalf + q4 * 32;
             T.col0 = U.tn * P.width + side * (P.width / 2);
             T.cols = T.row0 < P.M ? max(0, min(P.width / 2, P.N - T.col0)) : 0;
@@ -461,7 +484,7 @@ inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int
     P.width = width;
     P.ntn = (N + width - 1) / width;
     P.tiles = mm_tiles(P.ntm, P.ntn, sym, width);
-    P.chunk = 1 << 28;
+    P.chunk = kMmChunkAll;
     P.m_fast = m_fast ? 1 : 0;
     P.unit0 = unit0;
     const int total = P.nkb * parts;
@@ -483,7 +506,7 @@ inline cudaError_t mm_launch(const MmBatch<kMaxProbs> &G, const typename Epi::Pa
 {
     if (G.nunits == 0) return cudaSuccess;
     const void *fn = (const void *)mm_kernel<kBf16, kMaxProbs, Epi>;
-    cudaError_t e = ensure_dyn_smem(fn, kMmSmemBytes);
+    cudaError_t e = ensure_dyn_smem(fn, kMmSmemBytes<kMaxProbs>);
     if (e != cudaSuccess) return e;
     if (Epi::kManyRegs) {
         // the register split counts on this: with fewer at launch, setmaxnreg would wait for registers that do not exist
@@ -496,8 +519,18 @@ inline cudaError_t mm_launch(const MmBatch<kMaxProbs> &G, const typename Epi::Pa
     int pairs = 0;
     if ((e = mm_pairs(&pairs)) != cudaSuccess) return e;
     if (pairs > G.nunits) pairs = G.nunits;
-    mm_kernel<kBf16, kMaxProbs, Epi><<<2 * pairs, kMmThreads, kMmSmemBytes, s>>>(G, E);
-    return cudaGetLastError();
+    // programmatic serialisation: the set-up (barriers, tensor memory, records) may overlap the end of the kernel before
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = kMmSmemBytes<kMaxProbs>;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, mm_kernel<kBf16, kMaxProbs, Epi>, G, E);
 }
 
 // Host: waits for `s`, returns and clears this file's error code.

@@ -682,8 +682,8 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         mm_plan(P, g.n, g.n, g.m, false, B.nunits, g.ranges, parts, g.batch, true);
         P.a_mn = P.b_mn = g.wide ? 0 : 1;
         P.za = P.zb = xz;
-        ok = ok && mm_operand(&P.mA, false, P.a_mn, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
-        P.mB = P.mA;
+        ok = ok && mm_operand(&B.mA[B.n], false, P.a_mn, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
+        B.mB[B.n] = B.mA[B.n];
         O.kind = kPart;
         ok = ok && tmap_encode_3d(&O.mD, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + g.part, g.pn, g.n,
                                   (long)g.ranges * g.batch, (long)g.pn * 4, (long)g.n * g.pn * 4, 32, 32);
@@ -733,8 +733,8 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         OrthProb &O = E.p[B.n];
         mm_plan(P, g.n, g.n, g.n, false, B.nunits, 1, 3, g.batch, true, wq);
         P.za = P.zb = 2;
-        ok = ok && mm_operand(&P.mA, false, false, ws + x, g.n, g.n, g.pn, 2L * g.batch) &&
-             mm_operand(&P.mB, false, false, ws + y, g.n, g.n, g.pn, 2L * g.batch, wq / 2);
+        ok = ok && mm_operand(&B.mA[B.n], false, false, ws + x, g.n, g.n, g.pn, 2L * g.batch) &&
+             mm_operand(&B.mB[B.n], false, false, ws + y, g.n, g.n, g.pn, 2L * g.batch, wq / 2);
         O.kind = kSym;
         O.pn = g.pn;
         O.first = g.first;
@@ -791,8 +791,8 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         CUtensorMap mQ, mX;
         ok = ok && mm_operand(&mQ, false, false, ws + Q, g.n, g.n, g.pn, 2L * g.batch, g.wide ? kMmHalf : wo / 2) &&
              mm_operand(&mX, false, g.wide, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
-        P.mA = g.wide ? mQ : mX;
-        P.mB = g.wide ? mX : mQ;
+        B.mA[B.n] = g.wide ? mQ : mX;
+        B.mB[B.n] = g.wide ? mX : mQ;
         P.b_mn = g.wide ? 1 : 0;
         P.b_whole = g.wide ? 1 : 0;
         P.za = g.wide ? 2 : xz;
