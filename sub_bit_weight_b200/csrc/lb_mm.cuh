@@ -184,6 +184,22 @@ __device__ __forceinline__ uint32_t mm_idesc(bool bf16, bool a_mn, bool b_mn, in
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMmTile >> 4) << 24);
 }
 
+// One lane of the (converged) warp: code under it stays uniform to the compiler, so that the descriptors and barrier
+// addresses of the loops below live in uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// Bounded wait of a whole warp: every lane gets lane 0's answer, so the warp stays together.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *b, uint32_t parity, volatile int *abort, int *err, int code)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, abort, err, code));
+}
+
 struct MmUnit {
     int q;             // problem
     int b;             // product of its batch
@@ -275,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     extern __shared__ __align__(1024) unsigned char mm_raw[];
     const uint32_t raw_addr = smem_u32(mm_raw);
     MmSmem<kMaxProbs> &S = *reinterpret_cast<MmSmem<kMaxProbs> *>(mm_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     volatile int *abort = &S.abort;
@@ -319,13 +335,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         // cycles for a k block, and a shared-memory read is 30 of them.
         if (warp == 0 || warp == 2) {
             // ---------------- producers: warp 0 copies A, warp 2 B
-            if (lane == 0) {
+            {
                 const bool is_a = warp == 0;
                 unsigned char *const base = is_a ? S.A[0] : S.B[0];
                 const uint32_t full0 = map_rank(smem_u32(&S.full[0]), 0);
                 uint32_t s = 0, ph = 0;
                 bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 ; ++n) {
                     const MmUnit U = mm_unit(S.p, nprobs, u);
                     const MmProb &P = S.p[U.q];
                     const CUtensorMap *const map = is_a ? &G.mA[U.q] : &G.mB[U.q];
@@ -341,17 +357,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                     const int low = parts == 3 ? (is_a ? 0 : 1) : parts == 2 && (is_a == (P.b_whole != 0)) ? 0 : -1;
                     int seg = U.kb0 / nkb, kb = U.kb0 - seg * nkb;
                     for (int left = U.kb1 - U.kb0; left > 0; --left) {
-                        if (!(ok = mbar_wait(&S.empty[s], ph ^ 1, abort, err, 1))) break;
-                        if (is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
+                        if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
+                        const bool one = elect_one();
+                        if (one && is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
                         unsigned char *const dst = base + s * kMmOperand;
                         const uint32_t bar = full0 + s * 8;
                         const int k = kb * kMmBK, z = z0 + (seg == low ? 1 : 0);
-                        if (mn) {
-                            tma_load_3d_pair(dst, map, x0, k, z, bar);
+                        if (one) {
+                            tma_load_3d_pair(dst, map, mn ? x0 : k, mn ? k : x0, z, bar);
                             if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z, bar);
-                        } else {
-                            tma_load_3d_pair(dst, map, k, x0, z, bar);
                         }
+                        __syncwarp();
                         if (++kb == nkb) {
                             kb = 0;
                             ++seg;
@@ -372,10 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             }
         } else if (warp == 1) {
             // ---------------- MMA issuer (first CTA of the pair)
-            if (lane == 0 && rank == 0) {
+            if (rank == 0) {
                 uint32_t s = 0, ph = 0, acc = 0;   // stage, its phase, accumulators used
                 bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 ; ++n) {
                     const MmUnit U = mm_unit(S.p, nprobs, u);
                     const MmProb &P = S.p[U.q];
                     const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
@@ -387,26 +403,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                     const int chunk = P.chunk;
                     for (int left = U.kb1 - U.kb0; ok && left > 0; left -= chunk, ++acc) {
                         const int ab = acc & 1;
-                        if (!(ok = mbar_wait(&S.acce[ab], ((acc >> 1) & 1) ^ 1, abort, err, 2))) break;
+                        if (!(ok = mbar_wait_warp(&S.acce[ab], ((acc >> 1) & 1) ^ 1, abort, err, 2))) break;
                         tc_fence_after();
                         const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
                         uint32_t add = 0;
                         for (int i = min(left, chunk); i > 0; --i) {
-                            if (!(ok = mbar_wait(&S.full[s], ph, abort, err, 3))) break;
+                            if (!(ok = mbar_wait_warp(&S.full[s], ph, abort, err, 3))) break;
                             tc_fence_after();
                             const uint64_t da = da0 + s * (kMmOperand >> 4), db = db0 + s * (kMmOperand >> 4);
-                            tc_mma_f16_pair(dacc, da, db, idesc, add);
+                            if (elect_one()) {
+                                tc_mma_f16_pair(dacc, da, db, idesc, add);
 #pragma unroll
-                            for (int kk = 1; kk < kMmBK / 16; ++kk)
-                                tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, 1u);
-                            tc_commit_pair(&S.empty[s]);
+                                for (int kk = 1; kk < kMmBK / 16; ++kk)
+                                    tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, 1u);
+                                tc_commit_pair(&S.empty[s]);
+                            }
+                            __syncwarp();
                             add = 1;
                             if (++s == kMmStages) {
                                 s = 0;
                                 ph ^= 1;
                             }
                         }
-                        if (ok) tc_commit_pair(&S.accf[ab]);
+                        if (ok && elect_one()) tc_commit_pair(&S.accf[ab]);
+                        __syncwarp();
                     }
                 }
             }

@@ -277,13 +277,17 @@ struct OrthEpi {
             }
             return;
         }
-        // A symmetric n x n matrix: every element on or above the diagonal is computed once and written to both its
-        // places.  (The products of a polynomial's factors are symmetric only up to rounding, and a difference between
-        // the triangles would grow by q(0)^2 = 12 a step.)
+        // A symmetric n x n matrix, in 32 x 32 blocks: one above the diagonal is computed once and written to both its
+        // places, one on the diagonal takes its lower half from its upper.  (The products of a polynomial's factors are
+        // symmetric only up to rounding, and a difference between the triangles would grow by q(0)^2 = 12 a step.)
         const size_t plane = (size_t)P.N * O.pn;
         for (int c = 0; c < T.cols; c += 32) {
-            tmem_ld32(T.tmem + c, v);
             const int col0 = T.col0 + c;
+            if (col0 < T.row0) {
+                if (c + 32 < T.cols) load_c(O, P, U, row, col0 + 32, S.hi, S.lo);
+                continue;
+            }
+            tmem_ld32(T.tmem + c, v);
             float x[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -294,46 +298,64 @@ struct OrthEpi {
                                         O.beta * (__half2float(ch[j]) + __half2float(cl[j])));
             }
             if (c + 32 < T.cols) load_c(O, P, U, row, col0 + 32, S.hi, S.lo);
-            if (row >= P.M || col0 + 31 < row) continue;
-            put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, row, col0, P.N);
+            put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, T, col0, P.N);
             if (O.D2) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (col0 + i == row) x[i] += O.gamma;
-                put(x, O.D2 + (size_t)U.b * 2 * plane, plane, O.pn, row, col0, P.N);
+                put(x, O.D2 + (size_t)U.b * 2 * plane, plane, O.pn, T, col0, P.N);
             }
         }
     }
-    // 32 columns of a row: the elements on or above the diagonal, and their mirror images
-    static __device__ __forceinline__ void put(const float (&x)[32], __half *D, size_t plane, int pn, int row, int col0,
-                                               int n)
+    static __device__ __forceinline__ void put(const float (&x)[32], __half *D, size_t plane, int pn, const MmTileCtx &T,
+                                               int col0, int n)
     {
-        alignas(16) __half hi[32], lo[32];
+        constexpr uint32_t kPitch = 80;   // bytes between rows of the staged transpose
+        const int row = T.row0 + T.lane;
+        const bool diag = col0 == T.row0;
+        uint32_t w[2][16];   // the row's halves, two to a word
 #pragma unroll
-        for (int i = 0; i < 32; ++i) halves(x[i], hi[i], lo[i]);
-        if (col0 >= row) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (col0 + 8 * i < pn) {
-                    *reinterpret_cast<uint4 *>(D + (size_t)row * pn + col0 + 8 * i) = *reinterpret_cast<uint4 *>(hi + 8 * i);
-                    *reinterpret_cast<uint4 *>(D + plane + (size_t)row * pn + col0 + 8 * i) =
-                        *reinterpret_cast<uint4 *>(lo + 8 * i);
-                }
-        } else {   // the block on the diagonal
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col0 + i >= row && col0 + i < n) {
-                    D[(size_t)row * pn + col0 + i] = hi[i];
-                    D[plane + (size_t)row * pn + col0 + i] = lo[i];
-                }
+        for (int i = 0; i < 16; ++i) {
+            __half h0, l0, h1, l1;
+            halves(x[2 * i], h0, l0);
+            halves(x[2 * i + 1], h1, l1);
+            w[0][i] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
+            w[1][i] = (uint32_t)__half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (col0 + i > row && col0 + i < n) {
-                const size_t at = (size_t)(col0 + i) * pn + row;
-                D[at] = hi[i];
-                D[plane + at] = lo[i];
+        for (int p = 0; p < 2; ++p) {
+            __half *const Dp = D + p * plane;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)i * kPitch + 2 * T.lane),
+                             "h"((uint16_t)(i & 1 ? w[p][i >> 1] >> 16 : w[p][i >> 1]))
+                             : "memory");
+            __syncwarp();
+            uint4 t[4];   // column `lane` of the block
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = lds128(T.st + (uint32_t)T.lane * kPitch + 16 * i);
+            if (diag) {
+                const uint32_t *tw = reinterpret_cast<const uint32_t *>(t);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (2 * i < T.lane) w[p][i] = (w[p][i] & 0xffff0000u) | (tw[i] & 0xffffu);
+                    if (2 * i + 1 < T.lane) w[p][i] = (w[p][i] & 0xffffu) | (tw[i] & 0xffff0000u);
+                }
+            } else if (col0 + T.lane < n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (T.row0 + 8 * i < pn)
+                        *reinterpret_cast<uint4 *>(Dp + (size_t)(col0 + T.lane) * pn + T.row0 + 8 * i) = t[i];
             }
+            if (row < n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col0 + 8 * i < pn)
+                        *reinterpret_cast<uint4 *>(Dp + (size_t)row * pn + col0 + 8 * i) =
+                            make_uint4(w[p][4 * i], w[p][4 * i + 1], w[p][4 * i + 2], w[p][4 * i + 3]);
+            }
+        }
     }
 };
 
