@@ -310,7 +310,6 @@ struct OrthEpi {
     static __device__ __forceinline__ void put(const float (&x)[32], __half *D, size_t plane, int pn, const MmTileCtx &T,
                                                int col0, int n)
     {
-        constexpr uint32_t kPitch = 80;   // bytes between rows of the staged transpose
         const int row = T.row0 + T.lane;
         const bool diag = col0 == T.row0;
         uint32_t w[2][16];   // the row's halves, two to a word
@@ -322,39 +321,54 @@ struct OrthEpi {
             w[0][i] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
             w[1][i] = (uint32_t)__half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
         }
+        // The transposes: row i of a plane's 2 KB (64 bytes) is column i of the block; its four 16-byte chunks are
+        // permuted by the row, so that the 32 rows of a read fall on all banks.
+        __syncwarp();
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            __half *const Dp = D + p * plane;
-            __syncwarp();
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)i * kPitch + 2 * T.lane),
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t chunk = (uint32_t)((T.lane >> 3) ^ ((i >> 1) & 3));
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + 2048u * p + 64u * i + 16u * chunk + 2u * (T.lane & 7)),
                              "h"((uint16_t)(i & 1 ? w[p][i >> 1] >> 16 : w[p][i >> 1]))
                              : "memory");
-            __syncwarp();
-            uint4 t[4];   // column `lane` of the block
+            }
+        __syncwarp();
+        uint4 t[2][4];   // column `lane` of the block
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = lds128(T.st + (uint32_t)T.lane * kPitch + 16 * i);
-            if (diag) {
-                const uint32_t *tw = reinterpret_cast<const uint32_t *>(t);
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[p][i] = lds128(T.st + 2048u * p + 64u * T.lane + 16u * (uint32_t)(i ^ ((T.lane >> 1) & 3)));
+        if (diag) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t *tw = reinterpret_cast<const uint32_t *>(t[p]);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (2 * i < T.lane) w[p][i] = (w[p][i] & 0xffff0000u) | (tw[i] & 0xffffu);
                     if (2 * i + 1 < T.lane) w[p][i] = (w[p][i] & 0xffffu) | (tw[i] & 0xffff0000u);
                 }
-            } else if (col0 + T.lane < n) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (T.row0 + 8 * i < pn)
-                        *reinterpret_cast<uint4 *>(Dp + (size_t)(col0 + T.lane) * pn + T.row0 + 8 * i) = t[i];
             }
-            if (row < n) {
+        } else if (col0 + T.lane < n) {
+            __half *const dst = D + (size_t)(col0 + T.lane) * pn + T.row0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (col0 + 8 * i < pn)
-                        *reinterpret_cast<uint4 *>(Dp + (size_t)row * pn + col0 + 8 * i) =
-                            make_uint4(w[p][4 * i], w[p][4 * i + 1], w[p][4 * i + 2], w[p][4 * i + 3]);
-            }
+            for (int i = 0; i < 4; ++i)
+                if (T.row0 + 8 * i < pn) {
+                    *reinterpret_cast<uint4 *>(dst + 8 * i) = t[0][i];
+                    *reinterpret_cast<uint4 *>(dst + plane + 8 * i) = t[1][i];
+                }
+        }
+        if (row < n) {
+            __half *const dst = D + (size_t)row * pn + col0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col0 + 8 * i < pn) {
+                    *reinterpret_cast<uint4 *>(dst + 8 * i) =
+                        make_uint4(w[0][4 * i], w[0][4 * i + 1], w[0][4 * i + 2], w[0][4 * i + 3]);
+                    *reinterpret_cast<uint4 *>(dst + plane + 8 * i) =
+                        make_uint4(w[1][4 * i], w[1][4 * i + 1], w[1][4 * i + 2], w[1][4 * i + 3]);
+                }
         }
     }
 };
