@@ -6,14 +6,18 @@
 // elements.  The gradient reads M D elements and writes all V D (rows without
 // a token are zero), in a fixed order of additions:
 //
-//   1  the blocks 0 .. C-1 each sort up to 16,384 (id, position) pairs in
-//      shared memory (bitonic; the pairs are distinct, so the order is unique)
-//      while the other blocks write the zeros of the rows that no token names,
-//      most of the output in a real vocabulary;
-//   2  (C > 1) every pair finds its place among the other blocks' sorted runs;
-//   3  a block takes 32 consecutive pairs and 256 vectors of columns, adds the
-//      rows of each token in float32 and writes the tokens that lie inside its
-//      32 pairs; a token that crosses into other blocks (a frequent one)
+//   1  every (id, position) pair's place among the sorted pairs is the number
+//      of smaller ones, counted directly against up to 16,384 ids in shared
+//      memory (the pairs are distinct, so the order is unique): 8192^2
+//      comparisons are 4 us for the whole GPU and need no exchange between
+//      blocks, where a sort in one block took 20 us.  The same blocks write the
+//      zeros of the rows that no token names, most of the output in a real
+//      vocabulary;
+//   2  (more than 16,384 tokens) every pair finds its place among the other
+//      chunks' sorted runs;
+//   3  a block takes 8 or 32 consecutive pairs and 256 vectors of columns, adds
+//      the rows of each token in float32 and writes the tokens that lie inside
+//      its pairs; a token that crosses into other blocks (a frequent one)
 //      leaves float32 partial sums there;
 //   4  the partial sums of each crossing token are added in order.
 
@@ -26,8 +30,9 @@
 namespace lb {
 namespace {
 
-constexpr int kSortMost = 16384;    // pairs one block sorts (128 KB of shared memory)
-constexpr int kSumPairs = 32;       // sorted pairs one block of step 3 adds
+constexpr int kSortMost = 16384;    // ids of a chunk (64 KB of shared memory)
+constexpr int kZeroRows = 4096;     // rows a block looks after at a time
+constexpr int kOrderThreads = 512;  // of a block's 1024 threads, those that count while the others write zeros
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
@@ -76,70 +81,91 @@ __global__ void __launch_bounds__(256) lookup_kernel(const int64_t *__restrict__
     }
 }
 
-// ---- 1: sort, and zeros of the rows without a token
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// ---- 1: order, and zeros of the rows without a token
 // Pairs are (id << 32 | position); an id outside 0 .. V-1 sorts behind every other, as V.
-template <int N, typename TO>
-__global__ void __launch_bounds__(1024) sort_zero_kernel(const int64_t *__restrict__ ids, long long M, int V, int D,
-                                                         int nsort, int chunk, unsigned long long *__restrict__ pairs,
-                                                         TO *__restrict__ out)
+// `split` threads count for one pair, each a share of the chunk's ids.
+__global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restrict__ ids, long long M, int V,
+                                                          size_t row_bytes, int nchunks, int chunk, int split,
+                                                          unsigned long long *__restrict__ pairs,
+                                                          unsigned char *__restrict__ out)
 {
     extern __shared__ __align__(16) unsigned char e_raw[];
-    if ((int)blockIdx.x < nsort) {
-        unsigned long long *k = reinterpret_cast<unsigned long long *>(e_raw);
-        const long long base = (long long)blockIdx.x * chunk;
-        const int n = (int)min((long long)chunk, M - base);
-        int p2 = 32;
-        while (p2 < n) p2 <<= 1;
-        for (int i = threadIdx.x; i < p2; i += 1024) {
-            unsigned long long key = ~0ull;
-            if (i < n) {
-                const long long id = ids[base + i];
-                key = ((unsigned long long)(id >= 0 && id < V ? (uint32_t)id : (uint32_t)V) << 32) | (uint32_t)(base + i);
+    int *const k = reinterpret_cast<int *>(e_raw);
+    unsigned char *const seen = e_raw + ((chunk + 3) & ~3) * 4;
+    const int tid = threadIdx.x;
+    const int per = (int)(((long long)V + gridDim.x - 1) / gridDim.x);
+    const long long r0 = (long long)blockIdx.x * per, r1 = min((long long)V, r0 + per);   // rows of this block
+    const int first = (int)min((long long)kZeroRows, max(0LL, r1 - r0));
+    const bool wide = row_bytes % 16 == 0 && ((uintptr_t)out & 15) == 0;
+    // zeros in the rows [v0, v0 + rows) without a token, by the threads t, t + n, ...; 128 threads a row
+    auto zeros = [&](long long v0, int rows, int t, int n) {
+        for (int r = t >> 7; r < rows; r += n >> 7) {
+            if (seen[r]) continue;
+            unsigned char *const dst = out + (v0 + r) * row_bytes;
+            if (wide) {
+                for (size_t i = t & 127; i < row_bytes / 16; i += 128)
+                    reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (size_t i = t & 127; i < row_bytes / 2; i += 128) reinterpret_cast<uint16_t *>(dst)[i] = 0;
             }
-            k[i] = key;
         }
-        for (int size = 2; size <= p2; size <<= 1)
-            for (int step = size >> 1; step > 0; step >>= 1) {
-                // steps below 32 stay inside one warp's 64 consecutive pairs
-                if (step >= 32 || step == size >> 1) __syncthreads();
-                else __syncwarp();
-                for (int i = threadIdx.x; i < p2 >> 1; i += 1024) {
-                    const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-                    const unsigned long long a = k[lo], b = k[hi];
-                    if ((a > b) == ((lo & size) == 0)) {
-                        k[lo] = b;
-                        k[hi] = a;
-                    }
+    };
+    pdl_go();
+    for (int i = tid; i < first; i += 1024) seen[i] = 0;
+    for (int c = 0; c < nchunks; ++c) {
+        const long long base = (long long)c * chunk;
+        const int n = (int)min((long long)chunk, M - base), n4 = (n + 3) & ~3;
+        __syncthreads();
+        for (int i = tid; i < n4; i += 1024) {
+            long long id = i < n ? ids[base + i] : (long long)V;
+            if (id < 0 || id >= V) id = V;
+            k[i] = (int)id;
+            if (id >= r0 && id - r0 < first) seen[id - r0] = 1;
+        }
+        __syncthreads();
+        if (tid >= kOrderThreads) {   // the last chunk's flags are complete: write zeros beside the counting
+            if (c + 1 == nchunks) zeros(r0, first, tid - kOrderThreads, 1024 - kOrderThreads);
+            continue;
+        }
+        const int groups = kOrderThreads / split, part = tid % split;
+        const uint32_t mates = (split == 32 ? ~0u : (1u << split) - 1) << ((tid & 31) - part);   // of one pair
+        for (int i = blockIdx.x * groups + tid / split; i < n; i += gridDim.x * groups) {
+            const int id = k[i], at = i >> 2;
+            int count = 0;
+#pragma unroll 4
+            for (int j = part; j < n4 / 4; j += split) {
+                const int4 q = reinterpret_cast<const int4 *>(k)[j];
+                const int t = id + (j < at ? 1 : 0);   // an equal id at an earlier position is smaller
+                if (j != at) {
+                    count += (q.x < t) + (q.y < t) + (q.z < t) + (q.w < t);
+                } else {
+                    const int o = i & 3;
+                    count += (q.x < id + (o > 0)) + (q.y < id + (o > 1)) + (q.z < id + (o > 2)) + (q.w < id);
                 }
             }
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += 1024) pairs[base + i] = k[i];
-        return;
+            for (int o = split >> 1; o; o >>= 1) count += __shfl_xor_sync(mates, count, o);
+            if (part == 0)
+                pairs[base + count] = ((unsigned long long)(uint32_t)id << 32) | (uint32_t)(base + i);
+        }
     }
-    // rows [v0, v1) of the vocabulary belong to this block
-    const int nz = gridDim.x - nsort, b = blockIdx.x - nsort;
-    const int per = (V + nz - 1) / nz;
-    unsigned char *seen = e_raw;
-    for (long long v0 = (long long)b * per, end = min((long long)V, v0 + per); v0 < end; v0 += kSortMost) {
-        const int rows = (int)min((long long)kSortMost, end - v0);
-        for (int i = threadIdx.x; i < rows; i += 1024) seen[i] = 0;
+    if (nchunks == 0) {
         __syncthreads();
-#pragma unroll 4
-        for (long long i = threadIdx.x; i < M; i += 1024) {
+        zeros(r0, first, tid, 1024);
+    }
+    for (long long v0 = r0 + kZeroRows; v0 < r1; v0 += kZeroRows) {   // more rows than one set of flags
+        const int rows = (int)min((long long)kZeroRows, r1 - v0);
+        __syncthreads();
+        for (int i = tid; i < rows; i += 1024) seen[i] = 0;
+        __syncthreads();
+        for (long long i = tid; i < M; i += 1024) {
             const long long r = ids[i] - v0;
             if (r >= 0 && r < rows) seen[r] = 1;
         }
         __syncthreads();
-        Vec<TO, N> zero;
-#pragma unroll
-        for (int i = 0; i < N; ++i) zero.v[i] = 0;
-        const int nv = D / N;
-        for (int r = threadIdx.x >> 7; r < rows; r += 8) {   // 128 threads a row
-            if (seen[r]) continue;
-            Vec<TO, N> *dst = reinterpret_cast<Vec<TO, N> *>(out + (v0 + r) * (long long)D);
-            for (int i = threadIdx.x & 127; i < nv; i += 128) dst[i] = zero;
-        }
-        __syncthreads();
+        zeros(v0, rows, tid, 1024);
     }
 }
 
@@ -148,6 +174,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const unsigned long long *__
                                                     int chunk, unsigned long long *__restrict__ out)
 {
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    pdl_go();
+    pdl_wait();
     if (i >= M) return;
     const unsigned long long key = in[i];
     const int own = (int)(i / chunk);
@@ -166,17 +194,19 @@ __global__ void __launch_bounds__(256) merge_kernel(const unsigned long long *__
     out[at] = key;
 }
 
-// ---- 3: sums of 32 pairs.  A token whose pairs begin before or end after this block's leaves its sum in part[2 b]
+// ---- 3: sums of kPairs pairs.  A token whose pairs begin before or end after this block's leaves its sum in part[2 b]
 // (it began before; also a token that fills the block) or part[2 b + 1] (it begins here and goes on).
-template <typename TI, typename TO, int N>
+template <typename TI, typename TO, int N, int kPairs>
 __global__ void __launch_bounds__(256) sum_kernel(const unsigned long long *__restrict__ pairs, long long M, int V, int D,
                                                   const TI *__restrict__ dout, float scale, TO *__restrict__ out,
                                                   float *__restrict__ part)
 {
-    __shared__ unsigned long long k[kSumPairs + 2];   // the pair before, 32 pairs, the pair after (~0 where there is none)
-    const long long base = (long long)blockIdx.x * kSumPairs;
-    const int n = (int)min((long long)kSumPairs, M - base);
-    if (threadIdx.x < kSumPairs + 2) {
+    __shared__ unsigned long long k[kPairs + 2];   // the pair before, kPairs, the pair after (~0 where there is none)
+    const long long base = (long long)blockIdx.x * kPairs;
+    const int n = (int)min((long long)kPairs, M - base);
+    pdl_go();
+    pdl_wait();
+    if (threadIdx.x < kPairs + 2) {
         const long long i = base + (int)threadIdx.x - 1;
         k[threadIdx.x] = i >= 0 && i < M && (int)threadIdx.x <= n + 1 ? pairs[i] : ~0ull;
     }
@@ -187,7 +217,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const unsigned long long *__re
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
     int first = 0;   // first pair of the current token in this block
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     for (int i0 = 0; i0 < n; i0 += kAhead) {
         Vec<TI, N> x[kAhead];
 #pragma unroll
@@ -228,15 +258,16 @@ __global__ void __launch_bounds__(256) sum_kernel(const unsigned long long *__re
 }
 
 // ---- 4: a token that begins in block b's pairs and goes on past them
-template <typename TO, int N>
+template <typename TO, int N, int kPairs>
 __global__ void __launch_bounds__(256) join_kernel(const unsigned long long *__restrict__ pairs, long long M, int V, int D,
                                                    const float *__restrict__ part, float scale, TO *__restrict__ out)
 {
-    const long long b = blockIdx.x, lastp = (b + 1) * kSumPairs - 1;
+    pdl_wait();
+    const long long b = blockIdx.x, lastp = (b + 1) * kPairs - 1;
     if (lastp + 1 >= M) return;
     const uint32_t id = (uint32_t)(pairs[lastp] >> 32);
     if ((int)id >= V || (uint32_t)(pairs[lastp + 1] >> 32) != id) return;   // nothing goes on
-    if (b > 0 && (uint32_t)(pairs[b * kSumPairs - 1] >> 32) == id) return;  // it began before this block
+    if (b > 0 && (uint32_t)(pairs[b * kPairs - 1] >> 32) == id) return;     // it began before this block
     // last block that holds a pair of this token: pairs are sorted, so search for the first larger id
     long long lo = lastp + 1, hi = M;
     while (lo < hi) {
@@ -244,11 +275,11 @@ __global__ void __launch_bounds__(256) join_kernel(const unsigned long long *__r
         if ((uint32_t)(pairs[mid] >> 32) <= id) lo = mid + 1;
         else hi = mid;
     }
-    const long long e = (lo - 1) / kSumPairs;
+    const long long e = (lo - 1) / kPairs;
     const int c = blockIdx.y * 256 + threadIdx.x;
     if (c >= D / N) return;
     Vec<float, N> a = reinterpret_cast<const Vec<float, N> *>(part + (2 * b + 1) * D)[c];
-#pragma unroll 4
+#pragma unroll 8
     for (long long q = b + 1; q <= e; ++q) {
         const Vec<float, N> x = reinterpret_cast<const Vec<float, N> *>(part + 2 * q * D)[c];
 #pragma unroll
@@ -275,7 +306,7 @@ int vector_of(int D, int most, const void *a, size_t sa, const void *b, size_t s
 }
 
 struct EmbedPlan {
-    int nsort, chunk;
+    int nchunks, chunk, per;   // chunks of ids, pairs a block of step 3 takes
     long long nsum;
     size_t pairs, sorted, part, bytes;
 };
@@ -283,11 +314,12 @@ struct EmbedPlan {
 bool embed_plan(EmbedPlan &L, long long M, int V, int D)
 {
     if (M < 0 || V < 1 || D < 1 || M > (1LL << 31) - 1) return false;
-    // equal chunks: the largest block's sort is what the others wait for
     const long long c = M ? (M + kSortMost - 1) / kSortMost : 0;
-    L.nsort = (int)c;
+    L.nchunks = (int)c;
     L.chunk = c ? (int)((M + c - 1) / c) : 0;
-    L.nsum = (M + kSumPairs - 1) / kSumPairs;
+    // few tokens: more blocks, each with all its rows in flight at once; many: half as many partial sums per row
+    L.per = M <= 4096 ? 8 : 32;
+    L.nsum = (M + L.per - 1) / L.per;
     size_t at = 0;
     auto take = [&](size_t b) {
         const size_t o = at;
@@ -295,7 +327,7 @@ bool embed_plan(EmbedPlan &L, long long M, int V, int D)
         return o;
     };
     L.pairs = take((size_t)M * 8);
-    L.sorted = take(c > 1 ? (size_t)M * 8 : 0);
+    L.sorted = take(L.nchunks > 1 ? (size_t)M * 8 : 0);
     L.part = take((size_t)L.nsum * 2 * D * 4);
     L.bytes = at;
     return true;
@@ -322,6 +354,33 @@ cudaError_t lookup(int n, const int64_t *ids, long long M, const void *table, in
     return launch_lookup<TI, TO, 1>(ids, M, table, V, D, scale, out, s);
 }
 
+// A launch whose set-up may overlap the kernel before it (the kernel waits for it with griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+
+template <typename TI, typename TO, int N, int kPairs>
+cudaError_t launch_sums(const EmbedPlan &L, const unsigned long long *pairs, long long M, const void *dout, int V, int D,
+                        float scale, void *dtable, float *part, cudaStream_t s)
+{
+    const dim3 grid((unsigned)L.nsum, (D / N + 255) / 256);
+    const cudaError_t e = launch_after(sum_kernel<TI, TO, N, kPairs>, grid, s, pairs, M, V, D, (const TI *)dout, scale,
+                                       (TO *)dtable, part);
+    if (e != cudaSuccess) return e;
+    return launch_after(join_kernel<TO, N, kPairs>, grid, s, pairs, M, V, D, (const float *)part, scale, (TO *)dtable);
+}
+
 template <typename TI, typename TO, int N>
 cudaError_t launch_grad(const EmbedPlan &L, const int64_t *ids, long long M, const void *dout, int V, int D, float scale,
                         void *dtable, unsigned char *ws, cudaStream_t s, int *launches)
@@ -329,37 +388,37 @@ cudaError_t launch_grad(const EmbedPlan &L, const int64_t *ids, long long M, con
     int sms = 0;
     cudaError_t e = sm_count_of_current(&sms);
     if (e != cudaSuccess) return e;
-    // shared memory: the chunk's pairs, rounded up to a power of two, or the flags of a block's rows
-    size_t p2 = 32;
-    while (p2 < (size_t)L.chunk) p2 <<= 1;
-    const int nz = (int)std::min<long long>(V, std::max(sms - L.nsort, 32));
-    const size_t flags = std::min<size_t>((V + nz - 1) / nz, kSortMost);
-    const size_t smem = std::max(L.nsort ? p2 * 8 : 0, flags);
-    const void *fn = (const void *)sort_zero_kernel<N, TO>;
-    if ((e = ensure_dyn_smem(fn, smem)) != cudaSuccess) return e;
+    const int blocks = (int)std::min<long long>(sms, std::max<long long>(V, (M + 31) / 32));
+    int split = 1;   // threads per pair: as many as keep every thread busy
+    while (split < 32 && (long long)L.chunk * split * 2 <= (long long)blocks * kOrderThreads) split <<= 1;
+    const size_t smem = (size_t)((L.chunk + 3) & ~3) * 4 + kZeroRows;
+    if ((e = ensure_dyn_smem((const void *)order_zero_kernel, smem)) != cudaSuccess) return e;
     unsigned long long *pairs = (unsigned long long *)(ws + L.pairs);
-    sort_zero_kernel<N, TO><<<L.nsort + nz, 1024, smem, s>>>(ids, M, V, D, L.nsort, L.chunk, pairs, (TO *)dtable);
+    order_zero_kernel<<<blocks, 1024, smem, s>>>(ids, M, V, (size_t)D * sizeof(TO), L.nchunks, L.chunk, split, pairs,
+                                                 (unsigned char *)dtable);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launches;
-    if (M > 0) {
-        if (L.nsort > 1) {
-            unsigned long long *sorted = (unsigned long long *)(ws + L.sorted);
-            merge_kernel<<<(unsigned)((M + 255) / 256), 256, 0, s>>>(pairs, M, L.nsort, L.chunk, sorted);
-            pairs = sorted;
-            ++*launches;
-        }
-        float *part = (float *)(ws + L.part);
-        const dim3 grid((unsigned)L.nsum, (D / N + 255) / 256);
-        sum_kernel<TI, TO, N><<<grid, 256, 0, s>>>(pairs, M, V, D, (const TI *)dout, scale, (TO *)dtable, part);
-        join_kernel<TO, N><<<grid, 256, 0, s>>>(pairs, M, V, D, part, scale, (TO *)dtable);
-        *launches += 2;
+    if (M == 0) return cudaSuccess;
+    if (L.nchunks > 1) {
+        unsigned long long *sorted = (unsigned long long *)(ws + L.sorted);
+        e = launch_after(merge_kernel, dim3((unsigned)((M + 255) / 256)), s, (const unsigned long long *)pairs, M, L.nchunks,
+                         L.chunk, sorted);
+        if (e != cudaSuccess) return e;
+        pairs = sorted;
+        ++*launches;
     }
-    return cudaGetLastError();
+    *launches += 2;
+    float *const part = (float *)(ws + L.part);
+    return L.per == 8 ? launch_sums<TI, TO, N, 8>(L, pairs, M, dout, V, D, scale, dtable, part, s)
+                      : launch_sums<TI, TO, N, 32>(L, pairs, M, dout, V, D, scale, dtable, part, s);
 }
 
 template <typename TI, typename TO>
 cudaError_t grad(int n, const EmbedPlan &L, const int64_t *ids, long long M, const void *dout, int V, int D, float scale,
                  void *dtable, unsigned char *ws, cudaStream_t s, int *launches)
 {
+    if constexpr (sizeof(TI) == 2)
+        if (n == 8) return launch_grad<TI, TO, 8>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
     if (n == 4) return launch_grad<TI, TO, 4>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
     if (n == 2) return launch_grad<TI, TO, 2>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
     return launch_grad<TI, TO, 1>(L, ids, M, dout, V, D, scale, dtable, ws, s, launches);
@@ -412,7 +471,7 @@ extern "C" lb_status lb_embedding_backward(const int64_t *ids, int64_t M, const 
     if (M > 0 && (!ids || !dout || !workspace || misaligned(ids, 8) || misaligned(dout, si) ||
                   misaligned(workspace, 256) || workspace_bytes < L.bytes))
         return LB_ERR_INVALID_ARG;
-    const int n = vector_of(D, 4, M ? dout : dtable, M ? si : so, dtable, so);
+    const int n = vector_of(D, si == 2 ? 8 : 4, M ? dout : dtable, M ? si : so, dtable, so);
     unsigned char *ws = (unsigned char *)workspace;
     cudaStream_t s = (cudaStream_t)stream;
     int launches = 0;

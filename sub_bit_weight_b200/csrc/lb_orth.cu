@@ -29,7 +29,10 @@
 // bfloat16 G is scaled by a power of two, which makes its high half exact and
 // its low half zero: one product for A_0 instead of three, two for X_0 Q.
 //
-// Ranks up to 64 run the n x n part in one block per matrix, in float32 FMAs;
+// A matrix of at most 24,576 elements and rank at most 64 is done whole by one
+// block, in float32 from shared memory (one launch instead of five: 4 matrices
+// of 512 x 16 took 49 us in five).  Ranks up to 64 otherwise run the n x n part
+// in one block per matrix, in float32 FMAs;
 // larger ranks as launches over all matrices (three per step), on CTA pairs.
 
 #include <algorithm>
@@ -479,21 +482,10 @@ __device__ __forceinline__ void small_add(const float *D, int ty, int tx, float 
         for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a, D[(4 * ty + i) * kSmallP + 4 * tx + j], c[i][j]);
 }
 
-__global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
+// Q_steps from A (both 64 x kSmallP in shared memory; p and T are scratch); 256 threads, ends synchronised
+__device__ __forceinline__ void small_chain(float *A, float *p, float *T, float *Q, int n, int steps)
 {
-    extern __shared__ __align__(16) float sm[];
-    float *A = sm, *q = A + 64 * kSmallP, *T = q + 64 * kSmallP, *Q = T + 64 * kSmallP;
-    int w = 0;
-    for (int i = 1; i < P.n; ++i)
-        if ((int)blockIdx.x >= P.g[i].b0) w = i;
-    const GroupArg &g = P.g[w];
-    const int b = blockIdx.x - g.b0, n = g.n, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const float f = P.scal[g.first + b].y * (1.0f / kSA);
-    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
-        const int i = e >> 6, j = e & 63;
-        A[i * kSmallP + j] = i < n && j < n ? part_sum(g, b, i, j) * f : 0.0f;
-    }
-    __syncthreads();
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const bool mine = ty <= tx && 4 * tx < n;
     float c[4][4];
     for (int k = 0; k < steps; ++k) {
@@ -504,7 +496,7 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
 #pragma unroll
                 for (int j = 0; j < 4; ++j) c[i][j] *= kC;
             small_add(A, ty, tx, kB, c);
-            small_put(q, ty, tx, c);
+            small_put(p, ty, tx, c);
             if (k == 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -517,7 +509,7 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
         __syncthreads();
         if (k > 0) {
             if (mine) {
-                small_mul(Q, q, n, ty, tx, c);
+                small_mul(Q, p, n, ty, tx, c);
                 small_add(Q, ty, tx, kA, c);
             }
             __syncthreads();
@@ -525,19 +517,37 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
         }
         if (k + 1 < steps) {
             if (mine) {
-                small_mul(A, q, n, ty, tx, c);
+                small_mul(A, p, n, ty, tx, c);
                 small_add(A, ty, tx, kA, c);
                 small_put(T, ty, tx, c);
             }
             __syncthreads();
             if (mine) {
-                small_mul(T, q, n, ty, tx, c);
+                small_mul(T, p, n, ty, tx, c);
                 small_add(T, ty, tx, kA, c);
                 small_put(A, ty, tx, c);
             }
         }
         __syncthreads();
     }
+}
+
+__global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP;
+    int w = 0;
+    for (int i = 1; i < P.n; ++i)
+        if ((int)blockIdx.x >= P.g[i].b0) w = i;
+    const GroupArg &g = P.g[w];
+    const int b = blockIdx.x - g.b0, n = g.n;
+    const float f = P.scal[g.first + b].y * (1.0f / kSA);
+    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+        const int i = e >> 6, j = e & 63;
+        A[i * kSmallP + j] = i < n && j < n ? part_sum(g, b, i, j) * f : 0.0f;
+    }
+    __syncthreads();
+    small_chain(A, p, T, Q, n, steps);
     const size_t plane = (size_t)n * g.pn;
     __half *D = g.A + (size_t)b * 2 * plane;
     for (int e = threadIdx.x; e < 64 * 64; e += 256) {
@@ -548,6 +558,112 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
             D[(size_t)i * g.pn + j] = hi;
             D[plane + (size_t)i * g.pn + j] = lo;
         }
+    }
+}
+
+// ---- a whole small matrix in one block
+constexpr int kTinyElems = 24576;   // m times n rounded up to 4
+struct TinyMat {
+    const void *G;
+    uint16_t *O;
+    int rows, cols;
+};
+struct Tinies {
+    TinyMat m[kMostMats];
+    int bf16, steps;
+    float eps;
+};
+
+__global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinies P)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP, *X = Q + 64 * kSmallP;
+    __shared__ double sums[8];
+    const TinyMat &M = P.m[blockIdx.x];
+    const int rows = M.rows, cols = M.cols, tid = threadIdx.x;
+    const bool wide = rows < cols;
+    const int m = max(rows, cols), n = min(rows, cols), pitch = (n + 3) & ~3;   // X is m x n: G, or its transpose
+    const int total = rows * cols;
+
+    double s = 0.0;
+    for (int e = tid; e < m * pitch; e += 256)
+        if (e % pitch >= n) X[e] = 0.0f;
+#pragma unroll 4
+    for (int e = tid; e < total; e += 256) {
+        const float x = load_g(M.G, e, P.bf16);
+        const int r = e / cols, c = e - r * cols;
+        X[wide ? c * pitch + r : r * pitch + c] = x;
+        s += (double)x * x;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((tid & 31) == 0) sums[tid >> 5] = s;
+    for (int e = tid; e < 64 * kSmallP; e += 256) A[e] = 0.0f;
+    __syncthreads();
+    s = 0.0;
+    for (int i = 0; i < 8; ++i) s += sums[i];
+    const double norm = sqrt(s), f = norm == 0.0 ? 0.0 : 1.0 / (norm + (double)P.eps);
+    for (int e = tid; e < m * pitch; e += 256) X[e] = (float)(X[e] * f);
+    __syncthreads();
+
+    // A = X^T X: 4 x 4 tiles, the rows of X dealt to as many groups of threads as there are
+    {
+        const int td = pitch / 4, tiles = td * td, groups = 256 / tiles;
+        const int g = tid / tiles, t = tid - g * tiles, ty = t / td, tx = t - ty * td;
+        float c[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+        if (g < groups)
+#pragma unroll 4
+            for (int k = g; k < m; k += groups) {
+                const float4 x = *reinterpret_cast<const float4 *>(X + k * pitch + 4 * ty);
+                const float4 y = *reinterpret_cast<const float4 *>(X + k * pitch + 4 * tx);
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+            }
+        // the groups' sums in p, T and Q (at most 256 * 16 values), then added in order
+        float *const part = p;
+        if (g < groups)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4 *>(part + (g * pitch + 4 * ty + i) * pitch + 4 * tx) =
+                    make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+        __syncthreads();
+        for (int e = tid; e < pitch * pitch; e += 256) {
+            float a = 0.0f;
+            for (int i = 0; i < groups; ++i) a += part[i * pitch * pitch + e];
+            A[e / pitch * kSmallP + e % pitch] = a;
+        }
+        __syncthreads();
+    }
+    small_chain(A, p, T, Q, n, P.steps);
+
+    // the update, 4 columns of a row of X Q at a time
+    for (int e = tid; e < m * (pitch / 4); e += 256) {
+        const int i = e % m, j = e / m * 4;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float x = X[i * pitch + k];
+            const float4 q = *reinterpret_cast<const float4 *>(Q + k * kSmallP + j);
+            a.x = fmaf(x, q.x, a.x);
+            a.y = fmaf(x, q.y, a.y);
+            a.z = fmaf(x, q.z, a.z);
+            a.w = fmaf(x, q.w, a.w);
+        }
+        const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < n) {
+                uint16_t o;
+                asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(o) : "f"(v[u]));
+                M.O[wide ? (size_t)(j + u) * m + i : (size_t)i * n + j + u] = o;
+            }
     }
 }
 
@@ -565,12 +681,13 @@ struct Chunk {
     std::vector<int> order;
     std::vector<Group> groups;
     size_t sums, scal, bytes;
+    bool tiny;
 };
 
-double cost_of(int r, int c)
+bool is_tiny(int r, int c)
 {
-    const double n = std::min(r, c), m = std::max(r, c);
-    return n * n * (4 * m + 20 * n);
+    const long n = std::min(r, c), m = std::max(r, c);
+    return n <= kSmallN && m * ((n + 3) & ~3L) <= kTinyElems;
 }
 
 // Sets of at most kMostMats matrices and kMostGroups shapes, the longest units first in each.
@@ -580,6 +697,8 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
     for (int i = 0; i < count; ++i) idx[i] = i;
     std::sort(idx.begin(), idx.end(), [&](int a, int b) {
         const int na = std::min(rows[a], cols[a]), nb = std::min(rows[b], cols[b]);
+        const bool ta = is_tiny(rows[a], cols[a]), tb = is_tiny(rows[b], cols[b]);
+        if (ta != tb) return tb;
         if (na != nb) return na > nb;
         if (rows[a] != rows[b]) return rows[a] > rows[b];
         if (cols[a] != cols[b]) return cols[a] > cols[b];
@@ -587,8 +706,16 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
     });
     for (int at = 0; at < count;) {
         Chunk C;
+        C.tiny = is_tiny(rows[idx[at]], cols[idx[at]]);
+        C.bytes = 0;
         while (at < count && (int)C.order.size() < kMostMats) {
             const int i = idx[at];
+            if (is_tiny(rows[i], cols[i]) != C.tiny) break;
+            if (C.tiny) {
+                C.order.push_back(i);
+                ++at;
+                continue;
+            }
             if (C.groups.empty() || C.groups.back().rows != rows[i] || C.groups.back().cols != cols[i]) {
                 if ((int)C.groups.size() == kMostGroups) break;
                 Group g;
@@ -606,6 +733,10 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             ++C.groups.back().batch;
             C.order.push_back(i);
             ++at;
+        }
+        if (C.tiny) {
+            out.push_back(std::move(C));
+            continue;
         }
         // ranges of the Gram products: units of about a quarter of a pair's share, at least 24 k blocks (6 us)
         const int parts = bf16 ? 1 : 3;
@@ -845,6 +976,28 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     return status_from(cudaGetLastError());
 }
 
+lb_status tiny_chunk(const Chunk &C, const void *const *Gs, const int *rows, const int *cols, bool bf16, int steps, float eps,
+                     uint16_t *const *Os, cudaStream_t s, int *launches)
+{
+    Tinies T;
+    memset(&T, 0, sizeof(T));
+    T.bf16 = bf16 ? 1 : 0;
+    T.steps = steps;
+    T.eps = eps;
+    int most = 0;
+    for (size_t k = 0; k < C.order.size(); ++k) {
+        const int i = C.order[k], n = std::min(rows[i], cols[i]), m = std::max(rows[i], cols[i]);
+        T.m[k] = TinyMat{Gs[i], Os[i], rows[i], cols[i]};
+        most = std::max(most, m * ((n + 3) & ~3));
+    }
+    const size_t smem = (size_t)(4 * 64 * kSmallP + most) * sizeof(float);
+    const cudaError_t e = ensure_dyn_smem((const void *)tiny_kernel, smem);
+    if (e != cudaSuccess) return status_from(e);
+    tiny_kernel<<<(unsigned)C.order.size(), 256, smem, s>>>(T);
+    ++*launches;
+    return status_from(cudaGetLastError());
+}
+
 bool orth_shapes_ok(const int *rows, const int *cols, int n)
 {
     if (n < 0 || (n > 0 && (!rows || !cols))) return false;
@@ -897,8 +1050,10 @@ extern "C" lb_status lb_orthogonalise(const void *const *G, int dtype, const int
         if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
         int launches = 0;
         for (const Chunk &c : chunks) {
-            const lb_status st = orth_chunk(c, G, dtype == LB_BF16, steps, eps, O, (unsigned char *)workspace,
-                                            (cudaStream_t)stream, &launches);
+            const bool bf16 = dtype == LB_BF16;
+            cudaStream_t s = (cudaStream_t)stream;
+            const lb_status st = c.tiny ? tiny_chunk(c, G, rows, cols, bf16, steps, eps, O, s, &launches)
+                                        : orth_chunk(c, G, bf16, steps, eps, O, (unsigned char *)workspace, s, &launches);
             if (st != LB_OK) return st;
         }
         set_launch_count(launches);

@@ -516,34 +516,42 @@ _sig("lb_orthogonalise", _st, [ctypes.POINTER(_vp), _i] + [ctypes.POINTER(_i)] *
 _sig("lb_train_status", _st, [_vp])
 
 
-class _On:
-    """The device of a call's tensors and its stream made current, so that what the call allocates belongs there."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, **tensors):
-        dev = None
-        for name, t in tensors.items():
+
+class _On:
+    """The device of a call's tensors and its stream made current, so that what the call allocates belongs there.
+    (Small calls take a few microseconds: where the tensors are on the current device and no stream is given, nothing
+    is entered or left.)"""
+
+    __slots__ = ("device", "stream", "_guard")
+
+    def __init__(self, stream, tensors, names):
+        first = tensors[0]
+        if not isinstance(first, torch.Tensor):
+            raise TypeError(f"{names[0]} must be a CUDA tensor")
+        dev = self.device = first.device
+        for t, name in zip(tensors, names):
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
                 raise TypeError(f"{name} must be a CUDA tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-        self.device = dev
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, {names[0]} on {dev}")
         self._guard = None
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream is not None:
+        if stream is None:
+            if dev.index != torch.cuda.current_device():
+                self._guard = torch.cuda.device(dev)
+            self.stream = _raw_stream(dev.index)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
             if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+                raise ValueError(f"the stream is on {stream.device}, {names[0]} on {dev}")
             self._guard = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(dev)
-        self._stream = stream
+            self.stream = stream.cuda_stream
 
     def __enter__(self):
         if self._guard is not None:
             self._guard.__enter__()
-        self.stream = (self._stream or torch.cuda.current_stream()).cuda_stream
         return self
 
     def __exit__(self, *exc):
@@ -579,7 +587,7 @@ def lb_embedding_forward(ids: torch.Tensor, table: torch.Tensor, scale: float = 
         raise ValueError("table must be [V, D]")
     V, D = table.shape
     dtype = table.dtype if dtype is None else dtype
-    with _On(stream, ids=ids, table=table) as on:
+    with _On(stream, (ids, table), ("ids", "table")) as on:
         out = torch.empty((*ids.shape, D), dtype=dtype, device=on.device)
         _check(_lib.lb_embedding_forward(_dev(ids, torch.int64, "ids"), ids.numel(),
                                          _dev(table, table.dtype, "table"), _element(table.dtype, "table"), V, D,
@@ -600,7 +608,7 @@ def lb_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, scale: 
     if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
         raise ValueError("dout must be [*ids.shape, D]")
     M, D = ids.numel(), dout.shape[-1]
-    with _On(stream, ids=ids, dout=dout) as on:
+    with _On(stream, (ids, dout), ("ids", "dout")) as on:
         dtable = torch.empty((V, D), dtype=dtype, device=on.device)
         ws = _workspace(workspace, lb_embedding_backward_workspace_bytes(M, V, D), on)
         _check(_lib.lb_embedding_backward(_dev(ids, torch.int64, "ids"), M, _dev(dout, dout.dtype, "dout"),
@@ -630,7 +638,7 @@ def lb_cross_entropy_forward(H: torch.Tensor, W: torch.Tensor, labels: torch.Ten
     """Softmax cross entropy of z = H W^T without keeping z: (loss [M], lse [M]) float32, for bfloat16 H [M, D] and
     W [V, D] and int64 labels [M]; a label outside 0 .. V-1 (such as -100) gives loss 0."""
     M, D, V = _loss_shapes(H, W, labels)
-    with _On(stream, H=H, W=W, labels=labels) as on:
+    with _On(stream, (H, W, labels), ("H", "W", "labels")) as on:
         loss, lse = (torch.empty(M, dtype=torch.float32, device=on.device) for _ in range(2))
         ws = _workspace(workspace, lb_cross_entropy_forward_workspace_bytes(M, D, V), on)
         _check(_lib.lb_cross_entropy_forward(_dev(H, torch.bfloat16, "H"), _dev(W, torch.bfloat16, "W"),
@@ -647,7 +655,7 @@ def lb_cross_entropy_gradient(H: torch.Tensor, W: torch.Tensor, labels: torch.Te
     ``rows``: rows taken at a time (0: 8192), which bounds the workspace."""
     M, D, V = _loss_shapes(H, W, labels)
     _numel(weight, M, "weight")
-    with _On(stream, H=H, W=W, labels=labels, weight=weight) as on:
+    with _On(stream, (H, W, labels, weight), ("H", "W", "labels", "weight")) as on:
         loss = torch.empty(M, dtype=torch.float32, device=on.device)
         dH = torch.empty((M, D), dtype=torch.bfloat16, device=on.device)
         dW = torch.empty((V, D), dtype=torch.bfloat16, device=on.device) if head else None
@@ -680,7 +688,7 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
     dtype = G[0].dtype
     code = _element(dtype, "G")
     rows, cols = ((_i * n)(*[t.shape[k] for t in G]) for k in (0, 1))
-    with _On(stream, **{f"G[{i}]": t for i, t in enumerate(G)}) as on:
+    with _On(stream, G, [f"G[{i}]" for i in range(n)]) as on:
         out = [torch.empty(t.shape, dtype=torch.bfloat16, device=on.device) for t in G]
         need = int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code))
         ws = _workspace(workspace, need, on)
