@@ -81,9 +81,6 @@ __global__ void __launch_bounds__(256) lookup_kernel(const int64_t *__restrict__
     }
 }
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
 // ---- 1: order, and zeros of the rows without a token
 // Pairs are (id << 32 | position); an id outside 0 .. V-1 sorts behind every other, as V.
 // `split` threads count for one pair, each a share of the chunk's ids.
@@ -354,31 +351,15 @@ cudaError_t lookup(int n, const int64_t *ids, long long M, const void *table, in
     return launch_lookup<TI, TO, 1>(ids, M, table, V, D, scale, out, s);
 }
 
-// A launch whose set-up may overlap the kernel before it (the kernel waits for it with griddepcontrol.wait).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, cudaStream_t s, A... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
-}
-
 template <typename TI, typename TO, int N, int kPairs>
 cudaError_t launch_sums(const EmbedPlan &L, const unsigned long long *pairs, long long M, const void *dout, int V, int D,
                         float scale, void *dtable, float *part, cudaStream_t s)
 {
     const dim3 grid((unsigned)L.nsum, (D / N + 255) / 256);
-    const cudaError_t e = launch_after(sum_kernel<TI, TO, N, kPairs>, grid, s, pairs, M, V, D, (const TI *)dout, scale,
+    const cudaError_t e = launch_after(sum_kernel<TI, TO, N, kPairs>, grid, 256, s, pairs, M, V, D, (const TI *)dout, scale,
                                        (TO *)dtable, part);
     if (e != cudaSuccess) return e;
-    return launch_after(join_kernel<TO, N, kPairs>, grid, s, pairs, M, V, D, (const float *)part, scale, (TO *)dtable);
+    return launch_after(join_kernel<TO, N, kPairs>, grid, 256, s, pairs, M, V, D, (const float *)part, scale, (TO *)dtable);
 }
 
 template <typename TI, typename TO, int N>
@@ -401,7 +382,7 @@ cudaError_t launch_grad(const EmbedPlan &L, const int64_t *ids, long long M, con
     if (M == 0) return cudaSuccess;
     if (L.nchunks > 1) {
         unsigned long long *sorted = (unsigned long long *)(ws + L.sorted);
-        e = launch_after(merge_kernel, dim3((unsigned)((M + 255) / 256)), s, (const unsigned long long *)pairs, M, L.nchunks,
+        e = launch_after(merge_kernel, dim3((unsigned)((M + 255) / 256)), 256, s, (const unsigned long long *)pairs, M, L.nchunks,
                          L.chunk, sorted);
         if (e != cudaSuccess) return e;
         pairs = sorted;

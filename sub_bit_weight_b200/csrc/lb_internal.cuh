@@ -187,6 +187,22 @@ struct GemmDesc {
     const float *alpha;
 };
 lb_status gemm_at_b_batch(const GemmDesc *descs, int n, int *err, cudaStream_t s);
+// Launch whose set-up may overlap the end of the kernel before it on the stream.  `fn` has to call pdl_wait() before it
+// touches memory that kernel may still be using.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
 // Raise the dynamic shared-memory limit of kernel `fn` on the current device to at least `bytes` (never lowers
 // it; per device and kernel, thread-safe).
 cudaError_t ensure_dyn_smem(const void *fn, size_t bytes);
@@ -209,6 +225,10 @@ struct lb_stack {
 // Small device helpers
 // ---------------------------------------------------------------------------
 namespace lb {
+
+// Programmatic launches: wait for the kernel before this one to finish; let the kernel after this one come up.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_go() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 __device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1)

@@ -163,6 +163,51 @@ struct LogitEpi {
     }
 };
 
+// ---- few rows: the logits of one k range, transposed ([V][M]: the vocabulary is the 256-wide side of the tiles, the few
+// rows their columns), float32, for few_kernel to add up
+struct FewEpi {
+    static constexpr bool kManyRegs = false;
+    struct Params {
+        CUtensorMap mD;            // float32 [ranges][V][Mp]
+    };
+    struct State {
+        float z[kMmHalf / 2];
+    };
+    static __device__ __forceinline__ void begin(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &)
+    {
+    }
+    static __device__ __forceinline__ void take(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &T,
+                                                State &S, bool first, bool, bool &)
+    {
+#pragma unroll
+        for (int c = 0; c < kMmHalf / 2; c += 32) {
+            if (c >= T.cols) continue;
+            uint32_t v[32];
+            tmem_ld32(T.tmem + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S.z[c + i] = first ? __uint_as_float(v[i]) : S.z[c + i] + __uint_as_float(v[i]);
+        }
+    }
+    static __device__ __forceinline__ void end(const Params &E, const MmProb &, const MmUnit &U, const MmTileCtx &T,
+                                               State &S, bool &stored)
+    {
+#pragma unroll
+        for (int c = 0; c < kMmHalf / 2; c += 32) {
+            if (c >= T.cols) continue;
+            staging_free(stored, T.lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *z = S.z + c + 4 * i;
+                sts128(T.st + sw128(T.lane, i), make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]),
+                                                           __float_as_uint(z[2]), __float_as_uint(z[3])));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (T.lane == 0) tma_store_3d(&E.mD, T.col0 + c, T.row0, U.split, T.st);
+        }
+    }
+};
+
 // ---- lse (base 2) of a row from its tiles' statistics, by a group of kThreads threads (a warp, or a block)
 __device__ __forceinline__ float2 lse_merge(float2 a, float2 b)
 {
@@ -182,11 +227,61 @@ __device__ __forceinline__ float2 lse_warp(float2 a)
     return a;
 }
 
+// Few rows: statistics of 64 vocabulary entries for every row, from the ranges' logits, added in order.  A lane has a row
+// and eight entries (with 16 rows or fewer the other lanes of the warp share them), all their loads in flight at once.
+constexpr int kFewEntries = 64;
+__global__ void __launch_bounds__(256) few_kernel(const float *__restrict__ part, int ranges, int M, int V, int Mp,
+                                                  int row_lanes, const int64_t *__restrict__ labels,
+                                                  float2 *__restrict__ stat, float *__restrict__ target)
+{
+    __shared__ float2 all[8][32];
+    pdl_go();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = lane / row_lanes, subs = 32 / row_lanes;   // which of the lanes that share a row's entries
+    const int v0 = blockIdx.x * kFewEntries + warp * 8;
+    const size_t step = (size_t)V * Mp;
+    for (int m0 = 0; m0 < M; m0 += row_lanes) {
+        const int m = m0 + lane % row_lanes;
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = -INFINITY;
+        if (m < M) {
+            const float *p = part + (size_t)v0 * Mp + m;
+            for (int r = 0; r < ranges; ++r, p += step)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i % subs == sub && v0 + i < V) z[i] = r ? z[i] + p[i * Mp] : p[i * Mp];
+            const long long lab = labels[m] - v0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (lab == i && i % subs == sub && v0 + i < V) target[m] = z[i];
+        }
+        float top = z[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, z[i]);
+        const float ref = top * kLog2e, from = top == -INFINITY ? 0.0f : ref;
+        float2 s = make_float2(ref, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s.y += ex2(fmaf(z[i], kLog2e, -from));
+        for (int o = row_lanes; o < 32; o <<= 1)
+            s = lse_merge(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+        all[warp][lane] = s;
+        __syncthreads();
+        if (warp == 0 && sub == 0 && m < M) {
+            for (int i = 1; i < 8; ++i) s = lse_merge(s, all[i][lane]);
+            stat[(size_t)m * gridDim.x + blockIdx.x] = s;
+        }
+        __syncthreads();
+    }
+}
+
 __global__ void __launch_bounds__(256) lse_kernel(const float2 *__restrict__ stat, const float *__restrict__ target,
                                                   const int64_t *__restrict__ labels, int M, int V, int nst,
                                                   float *__restrict__ loss, float *__restrict__ lse)
 {
     const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    pdl_wait();
     if (row >= M) return;
     float2 a = make_float2(-INFINITY, 0.0f);
     for (int t = lane; t < nst; t += 32) a = lse_merge(a, stat[(size_t)row * nst + t]);
@@ -235,6 +330,8 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
                                                    float *__restrict__ loss)
 {
     const int row = blockIdx.y, chunk = blockIdx.x;
+    pdl_go();
+    pdl_wait();
     const long long lab = labels[row];
     const bool counts = lab >= 0 && lab < V;
     if (chunk == 0 && Hc) {
@@ -349,6 +446,7 @@ __global__ void __launch_bounds__(256) round_sum_kernel(const float4 *__restrict
                                                         size_t nvec, const float *__restrict__ wref,
                                                         uint4 *__restrict__ out)
 {
+    pdl_wait();
     const float f = *wref;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < nvec; i += (size_t)gridDim.x * 256) {
         float4 a = part[2 * i], b = part[2 * i + 1];
@@ -389,8 +487,32 @@ int dh_splits(int M, int D, int V, bool with_dW, int pairs)
     return best;
 }
 
+// A forward pass of at most 128 rows is bound by reading W.  With the rows as the 256-wide side of the tiles the tensor
+// cores multiply mostly zeros, and take longer than the reading (118 us at M = 16, D = 8192, V = 32000); so W is that
+// side, and the rows are the columns (as few as 32).  Its tiles (256 vocabulary entries) divide badly, 125 on 74 pairs take
+// as long as 148, which cutting k into ranges evens out; the ranges' logits have to be written, read and added.
+// In bytes a pair waits for: the longest list of units, and its share of the logits.
+int few_ranges(int M, int D, int V)
+{
+    if (M > kMmHalf) return 0;
+    const long pairs = 74, tiles = ((long)V + kMmTile - 1) / kMmTile, nkb = ((long)D + kMmBK - 1) / kMmBK;
+    long best = 1;
+    double best_cost = 0.0;
+    for (long s = 1; s <= 16 && s <= nkb; ++s) {
+        const double rounds = (double)((tiles * s + pairs - 1) / pairs), unit = (double)((nkb + s - 1) / s) * kMmBK * kMmTile * 2;
+        const double cost = rounds * unit + (double)s * M * V * 8 / pairs;
+        if (s == 1 || cost < 0.98 * best_cost) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    const long per = (nkb + best - 1) / best;   // as mm_plan cuts
+    return (int)((nkb + per - 1) / per);
+}
+
 struct LossPlan {
     int rows, npieces, ntn, nst, Vp, splits;
+    int ranges, Mp;   // forward pass of few rows: k ranges whose logits are written (0: not few), pitch of the logits
     size_t stat, target, wref, E, Hc, part, acc, bytes;   // workspace offsets
 };
 
@@ -409,9 +531,14 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
         at = up256(at + b);
         return o;
     };
+    if (!grad && (L.ranges = few_ranges(L.rows, D, V)) > 0) L.nst = (V + kFewEntries - 1) / kFewEntries;
     L.stat = take((size_t)L.rows * L.nst * sizeof(float2));
     L.target = take((size_t)L.rows * 4);
     L.wref = take(grad ? 4 : 0);
+    if (L.ranges) {
+        L.Mp = (L.rows + 3) & ~3;
+        L.part = take((size_t)L.ranges * V * L.Mp * 4);
+    }
     if (grad) {
         // the plan's pairs: those of the B200's 148 SMs, whatever the current device, so that the size is one number
         L.splits = dh_splits(L.rows, D, V, with_dW, 74);
@@ -427,6 +554,32 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
 
 bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
+// accumulators of equal lengths, at most kChunk k blocks
+void set_chunk(MmProb &P)
+{
+    const int chunks = (P.kb_per + kChunk - 1) / kChunk;
+    P.chunk = (P.kb_per + chunks - 1) / chunks;
+}
+
+lb_status few_logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, int M, int D, int V, unsigned char *ws,
+                     cudaStream_t s)
+{
+    MmBatch<1> G;
+    FewEpi::Params E;
+    memset(&G, 0, sizeof(G));
+    const int width = M <= 64 ? 64 : 128;
+    G.n = 1;
+    mm_plan(G.p[0], V, M, D, true, 0, L.ranges, 1, 1, false, width);
+    set_chunk(G.p[0]);
+    G.nunits = mm_units(G.p[0]);
+    if (!mm_operand(&G.mA[0], true, false, W, V, D, D) ||
+        !mm_operand(&G.mB[0], true, false, H, M, D, D, 1, width / 2) ||
+        !tmap_encode_3d(&E.mD, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.part, L.Mp, V, L.ranges, (long)L.Mp * 4,
+                        (long)V * L.Mp * 4, 32, 32))
+        return LB_ERR_INVALID_ARG;
+    return status_from(mm_launch<true, 1, FewEpi>(G, E, s));
+}
+
 lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const int64_t *labels, int M, int D, int V,
                  unsigned char *ws, bool keep, cudaStream_t s)
 {
@@ -434,7 +587,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     memset(&G, 0, sizeof(G));
     G.n = 1;
     mm_plan(G.p[0], M, V, D, true, 0, 1);
-    G.p[0].chunk = kChunk;
+    set_chunk(G.p[0]);
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.mA[0], true, false, H, M, D, D) || !mm_operand(&G.mB[0], true, false, W, V, D, D))
         return LB_ERR_INVALID_ARG;
@@ -517,8 +670,9 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     if (P.splits > 1) {
         const size_t nvec = (size_t)M * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
-        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.part), (size_t)tile_rows * D / 4, P.splits, nvec,
+        const cudaError_t r = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.part), (size_t)tile_rows * D / 4, P.splits, nvec,
                                               E.wref, (uint4 *)dH);
+        if (r != cudaSuccess) return status_from(r);
         ++*launches;
     }
     return status_from(cudaGetLastError());
@@ -561,12 +715,20 @@ extern "C" lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t 
     if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
     unsigned char *ws = (unsigned char *)workspace;
     cudaStream_t s = (cudaStream_t)stream;
-    const lb_status st = logits(L, H, W, labels, M, D, V, ws, false, s);
+    const lb_status st = L.ranges ? few_logits(L, H, W, M, D, V, ws, s) : logits(L, H, W, labels, M, D, V, ws, false, s);
     if (st != LB_OK) return st;
-    lse_kernel<<<(M + 7) / 8, 256, 0, s>>>((const float2 *)(ws + L.stat), (const float *)(ws + L.target), labels, M, V,
-                                           L.nst, loss, lse);
-    set_launch_count(2);
-    return status_from(cudaGetLastError());
+    cudaError_t e;
+    if (L.ranges) {
+        int row_lanes = 4;
+        while (row_lanes < 32 && row_lanes < M) row_lanes <<= 1;
+        e = launch_after(few_kernel, dim3(L.nst), 256, s, (const float *)(ws + L.part), L.ranges, M, V, L.Mp, row_lanes,
+                         labels, (float2 *)(ws + L.stat), (float *)(ws + L.target));
+        if (e != cudaSuccess) return status_from(e);
+    }
+    e = launch_after(lse_kernel, dim3((M + 7) / 8), 256, s, (const float2 *)(ws + L.stat), (const float *)(ws + L.target),
+                     labels, M, V, L.nst, loss, lse);
+    set_launch_count(L.ranges ? 3 : 2);
+    return status_from(e);
 }
 
 extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W, const int64_t *labels,
@@ -601,10 +763,11 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
         lb_status st = logits(L, Hp, W, labels + r0, m, D, V, ws, true, s);
         if (st != LB_OK) return st;
         const dim3 grid((L.Vp + kGradCols - 1) / kGradCols, m);
-        grad_kernel<<<grid, 256, 0, s>>>((uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
+        cudaError_t e = launch_after(grad_kernel, grid, 256, s, (uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
                                          (const float *)(ws + L.target), labels + r0, weight + r0,
                                          (const float *)(ws + L.wref), V, L.Vp, L.nst, D,
                                          (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0);
+        if (e != cudaSuccess) return status_from(e);
         launches += 2;
         st = products(L, W, m, D, V, dH + (size_t)r0 * D, dW, p == 0, ws, s, &launches);
         if (st != LB_OK) return st;
@@ -612,8 +775,9 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     if (dW && L.npieces > 1) {
         const size_t nvec = (size_t)V * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
-        round_sum_kernel<<<grid, 256, 0, s>>>((const float4 *)(ws + L.acc), 0, 1, nvec, (const float *)(ws + L.wref),
+        const cudaError_t e = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.acc), 0, 1, nvec, (const float *)(ws + L.wref),
                                               (uint4 *)dW);
+        if (e != cudaSuccess) return status_from(e);
         ++launches;
     }
     set_launch_count(launches);

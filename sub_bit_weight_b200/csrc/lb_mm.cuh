@@ -326,8 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     const uint32_t tmem = S.tmem_base;
     // Launched to overlap with the kernel before it (see mm_launch): what follows reads and writes memory that kernel
     // may still be using, so wait for it to finish; the next kernel may come up as soon as this one has got here.
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    pdl_wait();
+    pdl_go();
 
     if (warp < 4) {
         if constexpr (Epi::kManyRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kMmRegsFew));

@@ -451,14 +451,22 @@ __device__ __forceinline__ void small_mul(const float *X, const float *Y, int n,
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-    for (int k = 0; k < n; ++k) {
-        const float4 x = *reinterpret_cast<const float4 *>(X + k * kSmallP + 4 * ty);
-        const float4 y = *reinterpret_cast<const float4 *>(Y + k * kSmallP + 4 * tx);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    // four rows at a time (rows n .. are zero), so that their reads overlap
+    for (int k = 0; k < n; k += 4) {
+        float4 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int u = 0; u < 4; ++u) {
+            x[u] = *reinterpret_cast<const float4 *>(X + (k + u) * kSmallP + 4 * ty);
+            y[u] = *reinterpret_cast<const float4 *>(Y + (k + u) * kSmallP + 4 * tx);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+        for (int u = 0; u < 4; ++u) {
+            const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+        }
     }
 }
 
@@ -482,7 +490,8 @@ __device__ __forceinline__ void small_add(const float *D, int ty, int tx, float 
         for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a, D[(4 * ty + i) * kSmallP + 4 * tx + j], c[i][j]);
 }
 
-// Q_steps from A (both 64 x kSmallP in shared memory; p and T are scratch); 256 threads, ends synchronised
+// Q_steps from A (both 64 x kSmallP in shared memory; p and T are scratch); at least 256 threads,
+// ends synchronised
 __device__ __forceinline__ void small_chain(float *A, float *p, float *T, float *Q, int n, int steps)
 {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -563,6 +572,7 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
 
 // ---- a whole small matrix in one block
 constexpr int kTinyElems = 24576;   // m times n rounded up to 4
+constexpr int kTinyThreads = 1024;
 struct TinyMat {
     const void *G;
     uint16_t *O;
@@ -574,11 +584,11 @@ struct Tinies {
     float eps;
 };
 
-__global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinies P)
+__global__ void __launch_bounds__(kTinyThreads) tiny_kernel(const __grid_constant__ Tinies P)
 {
     extern __shared__ __align__(16) float sm[];
     float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP, *X = Q + 64 * kSmallP;
-    __shared__ double sums[8];
+    __shared__ double sums[32];
     const TinyMat &M = P.m[blockIdx.x];
     const int rows = M.rows, cols = M.cols, tid = threadIdx.x;
     const bool wide = rows < cols;
@@ -586,10 +596,10 @@ __global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinie
     const int total = rows * cols;
 
     double s = 0.0;
-    for (int e = tid; e < m * pitch; e += 256)
+    for (int e = tid; e < m * pitch; e += kTinyThreads)
         if (e % pitch >= n) X[e] = 0.0f;
-#pragma unroll 4
-    for (int e = tid; e < total; e += 256) {
+#pragma unroll 8
+    for (int e = tid; e < total; e += kTinyThreads) {
         const float x = load_g(M.G, e, P.bf16);
         const int r = e / cols, c = e - r * cols;
         X[wide ? c * pitch + r : r * pitch + c] = x;
@@ -598,17 +608,17 @@ __global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinie
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((tid & 31) == 0) sums[tid >> 5] = s;
-    for (int e = tid; e < 64 * kSmallP; e += 256) A[e] = 0.0f;
+    for (int e = tid; e < 64 * kSmallP; e += kTinyThreads) A[e] = 0.0f;
     __syncthreads();
     s = 0.0;
-    for (int i = 0; i < 8; ++i) s += sums[i];
+    for (int i = 0; i < kTinyThreads / 32; ++i) s += sums[i];
     const double norm = sqrt(s), f = norm == 0.0 ? 0.0 : 1.0 / (norm + (double)P.eps);
-    for (int e = tid; e < m * pitch; e += 256) X[e] = (float)(X[e] * f);
+    for (int e = tid; e < m * pitch; e += kTinyThreads) X[e] = (float)(X[e] * f);
     __syncthreads();
 
     // A = X^T X: 4 x 4 tiles, the rows of X dealt to as many groups of threads as there are
     {
-        const int td = pitch / 4, tiles = td * td, groups = 256 / tiles;
+        const int td = pitch / 4, tiles = td * td, groups = min(kTinyThreads / tiles, 3 * 64 * kSmallP / (pitch * pitch));
         const int g = tid / tiles, t = tid - g * tiles, ty = t / td, tx = t - ty * td;
         float c[4][4];
 #pragma unroll
@@ -626,7 +636,7 @@ __global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinie
 #pragma unroll
                     for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
             }
-        // the groups' sums in p, T and Q (at most 256 * 16 values), then added in order
+        // the groups' sums in p, T and Q, which are one array, then added in order
         float *const part = p;
         if (g < groups)
 #pragma unroll
@@ -634,8 +644,9 @@ __global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinie
                 *reinterpret_cast<float4 *>(part + (g * pitch + 4 * ty + i) * pitch + 4 * tx) =
                     make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
         __syncthreads();
-        for (int e = tid; e < pitch * pitch; e += 256) {
+        for (int e = tid; e < pitch * pitch; e += kTinyThreads) {
             float a = 0.0f;
+#pragma unroll 4
             for (int i = 0; i < groups; ++i) a += part[i * pitch * pitch + e];
             A[e / pitch * kSmallP + e % pitch] = a;
         }
@@ -644,7 +655,7 @@ __global__ void __launch_bounds__(256) tiny_kernel(const __grid_constant__ Tinie
     small_chain(A, p, T, Q, n, P.steps);
 
     // the update, 4 columns of a row of X Q at a time
-    for (int e = tid; e < m * (pitch / 4); e += 256) {
+    for (int e = tid; e < m * (pitch / 4); e += kTinyThreads) {
         const int i = e % m, j = e / m * 4;
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
@@ -993,7 +1004,7 @@ lb_status tiny_chunk(const Chunk &C, const void *const *Gs, const int *rows, con
     const size_t smem = (size_t)(4 * 64 * kSmallP + most) * sizeof(float);
     const cudaError_t e = ensure_dyn_smem((const void *)tiny_kernel, smem);
     if (e != cudaSuccess) return status_from(e);
-    tiny_kernel<<<(unsigned)C.order.size(), 256, smem, s>>>(T);
+    tiny_kernel<<<(unsigned)C.order.size(), kTinyThreads, smem, s>>>(T);
     ++*launches;
     return status_from(cudaGetLastError());
 }

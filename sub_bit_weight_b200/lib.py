@@ -519,6 +519,16 @@ _sig("lb_train_status", _st, [_vp])
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+class _Names:
+    """Names of the entries of a list argument, made only where an error asks for one."""
+
+    def __init__(self, name):
+        self._name = name
+
+    def __getitem__(self, i):
+        return f"{self._name}[{i}]"
+
+
 class _On:
     """The device of a call's tensors and its stream made current, so that what the call allocates belongs there.
     (Small calls take a few microseconds: where the tensors are on the current device and no stream is given, nothing
@@ -531,11 +541,11 @@ class _On:
         if not isinstance(first, torch.Tensor):
             raise TypeError(f"{names[0]} must be a CUDA tensor")
         dev = self.device = first.device
-        for t, name in zip(tensors, names):
+        for i, t in enumerate(tensors):
             if not isinstance(t, torch.Tensor) or not t.is_cuda:
-                raise TypeError(f"{name} must be a CUDA tensor")
+                raise TypeError(f"{names[i]} must be a CUDA tensor")
             if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, {names[0]} on {dev}")
+                raise ValueError(f"{names[i]} is on {t.device}, {names[0]} on {dev}")
         self._guard = None
         if stream is None:
             if dev.index != torch.cuda.current_device():
@@ -682,17 +692,19 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
     n = len(G)
     if n == 0:
         return []
-    for i, t in enumerate(G):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.numel() == 0:
+    shapes = [t.shape if isinstance(t, torch.Tensor) else () for t in G]
+    for i, shape in enumerate(shapes):
+        if len(shape) != 2 or 0 in shape:
             raise ValueError(f"G[{i}] must be a matrix with at least one element")
-    dtype = G[0].dtype
+    dtype, names = G[0].dtype, _Names("G")
     code = _element(dtype, "G")
-    rows, cols = ((_i * n)(*[t.shape[k] for t in G]) for k in (0, 1))
-    with _On(stream, G, [f"G[{i}]" for i in range(n)]) as on:
-        out = [torch.empty(t.shape, dtype=torch.bfloat16, device=on.device) for t in G]
-        need = int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code))
-        ws = _workspace(workspace, need, on)
-        _check(_lib.lb_orthogonalise((_vp * n)(*[_dev(t, dtype, f"G[{i}]") for i, t in enumerate(G)]), code, rows, cols, n,
-                                     int(steps), float(eps), (_vp * n)(*[t.data_ptr() for t in out]),
-                                     _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream), "lb_orthogonalise")
+    rows, cols = (_i * n)(*[r for r, _ in shapes]), (_i * n)(*[c for _, c in shapes])
+    with _On(stream, G, names) as on:
+        src = (_vp * n)(*[t.data_ptr() if t.dtype is dtype and t.is_contiguous() else _dev(t, dtype, names[i])
+                          for i, t in enumerate(G)])
+        out = [torch.empty(shape, dtype=torch.bfloat16, device=on.device) for shape in shapes]
+        ws = _workspace(workspace, int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code)), on)
+        _check(_lib.lb_orthogonalise(src, code, rows, cols, n, int(steps), float(eps),
+                                     (_vp * n)(*[t.data_ptr() for t in out]), _dev(ws, torch.uint8, "workspace"),
+                                     ws.numel(), on.stream), "lb_orthogonalise")
     return out
