@@ -190,25 +190,51 @@ struct OrthEpi {
         uint16_t *out[kMostMats];
         const float2 *scal;
     };
+    // A warp's 32 x 32 block of a symmetric matrix (two planes of binary16) moves between memory and registers through
+    // its staging block, so that four lanes touch the 64 bytes of a row together: a lane that walks its own row alone
+    // makes four times as many requests to L2, which slowed the operands' copies to half.
     struct State {
-        uint4 hi[4], lo[4];   // kSym: the first 32 elements of C
+        uint4 c[2][4];   // kSym: the first block of C; part i of a lane is chunk lane % 4 of row 8 i + lane / 4
     };
-    static __device__ __forceinline__ void load_c(const OrthProb &O, const MmProb &P, const MmUnit &U, int row, int col,
-                                                  uint4 (&hi)[4], uint4 (&lo)[4])
+    // 16-byte chunk `chunk` of row `row` of plane p in the staging block: 64-byte rows, chunks permuted by the row so
+    // that eight rows fall on all banks
+    static __device__ __forceinline__ uint32_t stage(uint32_t st, int p, int row, int chunk)
+    {
+        return st + 2048u * p + 64u * row + 16u * (uint32_t)(chunk ^ ((row >> 1) & 3));
+    }
+    static __device__ __forceinline__ void load_c(const OrthProb &O, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
+                                                  int col0, State &S)
     {
         const size_t plane = (size_t)P.N * O.pn;
+        const int row = T.row0 + (T.lane >> 2), col = col0 + 8 * (T.lane & 3);
         const __half *C = O.C + (size_t)U.b * 2 * plane + (size_t)row * O.pn + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool in = row < P.M && col + 8 * i < O.pn && col + 31 >= row;
-            hi[i] = in ? *reinterpret_cast<const uint4 *>(C + 8 * i) : make_uint4(0, 0, 0, 0);
-            lo[i] = in ? *reinterpret_cast<const uint4 *>(C + plane + 8 * i) : make_uint4(0, 0, 0, 0);
+            const bool in = row + 8 * i < P.M && col < O.pn && col0 >= T.row0;
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                S.c[p][i] = in ? *reinterpret_cast<const uint4 *>(C + p * plane + (size_t)(8 * i) * O.pn)
+                               : make_uint4(0, 0, 0, 0);
         }
+    }
+    // the staged block to rows row0 .. and columns col0 .. of both planes of D
+    static __device__ __forceinline__ void write_block(uint32_t st, int lane, __half *D, size_t plane, int pn, int row0,
+                                                       int col0, int n)
+    {
+        const int row = row0 + (lane >> 2), col = col0 + 8 * (lane & 3);
+        __half *dst = D + (size_t)row * pn + col;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const uint4 v = lds128(stage(st, p, 8 * i + (lane >> 2), lane & 3));
+                if (row + 8 * i < n && col < pn) *reinterpret_cast<uint4 *>(dst + p * plane + (size_t)(8 * i) * pn) = v;
+            }
     }
     static __device__ __forceinline__ void begin(const Params &E, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
                                                  State &S)
     {
-        if (E.p[U.q].kind == kSym && T.cols > 0) load_c(E.p[U.q], P, U, T.row0 + T.lane, T.col0, S.hi, S.lo);
+        if (E.p[U.q].kind == kSym && T.cols > 0) load_c(E.p[U.q], P, U, T, T.col0, S);
     }
     static __device__ __forceinline__ void end(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &,
                                                bool &)
@@ -287,20 +313,27 @@ struct OrthEpi {
         for (int c = 0; c < T.cols; c += 32) {
             const int col0 = T.col0 + c;
             if (col0 < T.row0) {
-                if (c + 32 < T.cols) load_c(O, P, U, row, col0 + 32, S.hi, S.lo);
+                if (c + 32 < T.cols) load_c(O, P, U, T, col0 + 32, S);
                 continue;
             }
+            __syncwarp();
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sts128(stage(T.st, p, 8 * i + (T.lane >> 2), T.lane & 3), S.c[p][i]);
+            if (c + 32 < T.cols) load_c(O, P, U, T, col0 + 32, S);
             tmem_ld32(T.tmem + c, v);
+            __syncwarp();
             float x[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half *ch = reinterpret_cast<const __half *>(&S.hi[i]), *cl = reinterpret_cast<const __half *>(&S.lo[i]);
+                const uint4 h = lds128(stage(T.st, 0, T.lane, i)), l = lds128(stage(T.st, 1, T.lane, i));
+                const __half *ch = reinterpret_cast<const __half *>(&h), *cl = reinterpret_cast<const __half *>(&l);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     x[8 * i + j] = fmaf(__uint_as_float(v[8 * i + j]), O.alpha,
                                         O.beta * (__half2float(ch[j]) + __half2float(cl[j])));
             }
-            if (c + 32 < T.cols) load_c(O, P, U, row, col0 + 32, S.hi, S.lo);
             put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, T, col0, P.N);
             if (O.D2) {
 #pragma unroll
@@ -313,8 +346,6 @@ struct OrthEpi {
     static __device__ __forceinline__ void put(const float (&x)[32], __half *D, size_t plane, int pn, const MmTileCtx &T,
                                                int col0, int n)
     {
-        const int row = T.row0 + T.lane;
-        const bool diag = col0 == T.row0;
         uint32_t w[2][16];   // the row's halves, two to a word
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -324,55 +355,40 @@ struct OrthEpi {
             w[0][i] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
             w[1][i] = (uint32_t)__half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
         }
-        // The transposes: row i of a plane's 2 KB (64 bytes) is column i of the block; its four 16-byte chunks are
-        // permuted by the row, so that the 32 rows of a read fall on all banks.
+        // the transpose
         __syncwarp();
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t chunk = (uint32_t)((T.lane >> 3) ^ ((i >> 1) & 3));
-                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + 2048u * p + 64u * i + 16u * chunk + 2u * (T.lane & 7)),
+            for (int i = 0; i < 32; ++i)
+                asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(stage(T.st, p, i, T.lane >> 3) + 2u * (T.lane & 7)),
                              "h"((uint16_t)(i & 1 ? w[p][i >> 1] >> 16 : w[p][i >> 1]))
                              : "memory");
-            }
         __syncwarp();
-        uint4 t[2][4];   // column `lane` of the block
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                t[p][i] = lds128(T.st + 2048u * p + 64u * T.lane + 16u * (uint32_t)(i ^ ((T.lane >> 1) & 3)));
-        if (diag) {
+        if (col0 == T.row0) {   // on the diagonal: the lower half from the upper
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const uint32_t *tw = reinterpret_cast<const uint32_t *>(t[p]);
+                uint4 t[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = lds128(stage(T.st, p, T.lane, i));
+                const uint32_t *tw = reinterpret_cast<const uint32_t *>(t);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     if (2 * i < T.lane) w[p][i] = (w[p][i] & 0xffff0000u) | (tw[i] & 0xffffu);
                     if (2 * i + 1 < T.lane) w[p][i] = (w[p][i] & 0xffffu) | (tw[i] & 0xffff0000u);
                 }
             }
-        } else if (col0 + T.lane < n) {
-            __half *const dst = D + (size_t)(col0 + T.lane) * pn + T.row0;
+        } else {
+            write_block(T.st, T.lane, D, plane, pn, col0, T.row0, n);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (T.row0 + 8 * i < pn) {
-                    *reinterpret_cast<uint4 *>(dst + 8 * i) = t[0][i];
-                    *reinterpret_cast<uint4 *>(dst + plane + 8 * i) = t[1][i];
-                }
-        }
-        if (row < n) {
-            __half *const dst = D + (size_t)row * pn + col0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (col0 + 8 * i < pn) {
-                    *reinterpret_cast<uint4 *>(dst + 8 * i) =
-                        make_uint4(w[0][4 * i], w[0][4 * i + 1], w[0][4 * i + 2], w[0][4 * i + 3]);
-                    *reinterpret_cast<uint4 *>(dst + plane + 8 * i) =
-                        make_uint4(w[1][4 * i], w[1][4 * i + 1], w[1][4 * i + 2], w[1][4 * i + 3]);
-                }
-        }
+                sts128(stage(T.st, p, T.lane, i), make_uint4(w[p][4 * i], w[p][4 * i + 1], w[p][4 * i + 2], w[p][4 * i + 3]));
+        __syncwarp();
+        write_block(T.st, T.lane, D, plane, pn, T.row0, col0, n);
     }
 };
 
