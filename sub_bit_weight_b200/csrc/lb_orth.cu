@@ -168,6 +168,14 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats
     }
 }
 
+// two accumulators times f, as bfloat16
+__device__ __forceinline__ uint32_t pack_bf(uint32_t a, uint32_t b, float f)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(__uint_as_float(b) * f), "f"(__uint_as_float(a) * f));
+    return r;
+}
+
 // ---- products
 enum { kPart = 0, kSym = 1, kOut = 2 };
 constexpr int kMostProbs = 2 * kMostGroups;
@@ -269,40 +277,56 @@ struct OrthEpi {
             uint16_t *const base = E.out[O.first + U.b];
             const float f = O.alpha * E.scal[O.first + U.b].x;
             const bool vec = O.ldo % 8 == 0 && ((uintptr_t)base & 15) == 0;
+            if (vec) {   // 64 columns at a time through the staging block, eight lanes to the 128 bytes of a row
+                for (int c = 0; c < T.cols; c += 64) {
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h && c + 32 >= T.cols) break;
+                        tmem_ld32(T.tmem + c + 32 * h, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sts128(T.st + sw128(T.lane, 4 * h + i),
+                                   make_uint4(pack_bf(v[8 * i], v[8 * i + 1], f), pack_bf(v[8 * i + 2], v[8 * i + 3], f),
+                                              pack_bf(v[8 * i + 4], v[8 * i + 5], f), pack_bf(v[8 * i + 6], v[8 * i + 7], f)));
+                    }
+                    __syncwarp();
+                    const int r0 = T.lane >> 3, col = c + 8 * (T.lane & 7);
+                    uint16_t *dst = base + (size_t)(T.row0 + r0) * O.ldo + T.col0 + col;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 y = lds128(T.st + sw128(r0 + 4 * i, T.lane & 7));
+                        if (T.row0 + r0 + 4 * i < P.M && col < T.cols)
+                            *reinterpret_cast<uint4 *>(dst + (size_t)(4 * i) * O.ldo) = y;
+                    }
+                }
+                return;
+            }
+            // rows without alignment: through the staging block (32 rows of 32, 66 bytes apart), then one row of 32
+            // columns at a time
             for (int c = 0; c < T.cols; c += 32) {
                 tmem_ld32(T.tmem + c, v);
-                uint32_t w[16];
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n"
-                        : "=r"(w[i])
-                        : "f"(__uint_as_float(v[2 * i + 1]) * f), "f"(__uint_as_float(v[2 * i]) * f));
-                if (vec) {
-                    uint16_t *dst = base + (size_t)row * O.ldo + T.col0 + c;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (row < P.M && c + 8 * i < T.cols)
-                            *reinterpret_cast<uint4 *>(dst + 8 * i) =
-                                make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                } else {
-                    // rows without alignment: through the staging block (32 rows of 32, 66 bytes apart), then one row
-                    // of 32 columns at a time
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)(T.lane * 66 + 2 * i)),
-                                     "h"((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]))
-                                     : "memory");
-                    __syncwarp();
-                    const int rows = min(32, P.M - T.row0);
-                    uint16_t *dst = base + (size_t)T.row0 * O.ldo + T.col0 + c + T.lane;
-                    if (c + T.lane < T.cols)
-                        for (int r = 0; r < rows; ++r) {
-                            uint16_t y;
-                            asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(y) : "r"(T.st + (uint32_t)(r * 66 + 2 * T.lane)));
-                            dst[(size_t)r * O.ldo] = y;
-                        }
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t w = pack_bf(v[2 * i], v[2 * i + 1], f);
+                    asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)(T.lane * 66 + 4 * i)),
+                                 "h"((uint16_t)w)
+                                 : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(T.st + (uint32_t)(T.lane * 66 + 4 * i + 2)),
+                                 "h"((uint16_t)(w >> 16))
+                                 : "memory");
                 }
+                __syncwarp();
+                const int rows = min(32, P.M - T.row0);
+                uint16_t *dst = base + (size_t)T.row0 * O.ldo + T.col0 + c + T.lane;
+                if (c + T.lane < T.cols)
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r) {
+                        uint16_t y;
+                        asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(y) : "r"(T.st + (uint32_t)(r * 66 + 2 * T.lane)));
+                        dst[(size_t)r * O.ldo] = y;
+                    }
             }
             return;
         }
