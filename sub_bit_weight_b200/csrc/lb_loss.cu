@@ -36,7 +36,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kEScale = 15.0f;        // e is stored times 2^15
 constexpr int kChunk = 16;             // k blocks (1024 k) of logits one accumulator takes, see lb_mm.cuh
-constexpr int kGradCols = 8192;         // entries of a row one block of the second step takes
+constexpr int kGradCols = 8192;         // entries of a row one block of the second step takes, or up to four times that
 constexpr int kRowsDefault = 8192, kRowsMost = 32768;
 
 __device__ __forceinline__ float ex2(float x)
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
                                                    const float *__restrict__ weight,
                                                    const float *__restrict__ wref, int V, int Vp, int nst, int D,
                                                    const uint4 *__restrict__ H, uint4 *__restrict__ Hc,
-                                                   float *__restrict__ loss)
+                                                   float *__restrict__ loss, int cols)
 {
     const int row = blockIdx.y, chunk = blockIdx.x;
     pdl_go();
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
         const size_t base = (size_t)row * nv;
         for (int i = threadIdx.x; i < nv; i += 256) Hc[base + i] = counts ? H[base + i] : make_uint4(0, 0, 0, 0);
     }
-    const int v0 = chunk * (kGradCols / 8), v1 = min(Vp / 8, v0 + kGradCols / 8);   // vectors of 8 entries
+    const int v0 = chunk * (cols / 8), v1 = min(Vp / 8, v0 + cols / 8);   // vectors of 8 entries
     uint4 *out = E + (size_t)row * (Vp / 8);
     if (!counts) {
         for (int i = v0 + threadIdx.x; i < v1; i += 256) out[i] = make_uint4(0, 0, 0, 0);
@@ -524,7 +524,7 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
     L.npieces = M ? (M + L.rows - 1) / L.rows : 0;
     L.ntn = (V + kMmTile - 1) / kMmTile;
     L.nst = (V + kMmHalf - 1) / kMmHalf;
-    L.Vp = (V + 7) & ~7;
+    L.Vp = (V + 63) & ~63;   // rows of e begin on 128-byte lines: 16 bytes off, every store splits its sectors
     size_t at = 0;
     auto take = [&](size_t b) {
         const size_t o = at;
@@ -762,11 +762,14 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
         const uint16_t *Hp = H + (size_t)r0 * D;
         lb_status st = logits(L, Hp, W, labels + r0, m, D, V, ws, true, s);
         if (st != LB_OK) return st;
-        const dim3 grid((L.Vp + kGradCols - 1) / kGradCols, m);
+        // every block adds up its row's statistics first: as long a part of the row as leaves the GPU full of blocks
+        int cols = kGradCols;
+        while (cols < 4 * kGradCols && (long)m * ((L.Vp + 2 * cols - 1) / (2 * cols)) >= 148 * 8) cols *= 2;
+        const dim3 grid((L.Vp + cols - 1) / cols, m);
         cudaError_t e = launch_after(grad_kernel, grid, 256, s, (uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
                                          (const float *)(ws + L.target), labels + r0, weight + r0,
                                          (const float *)(ws + L.wref), V, L.Vp, L.nst, D,
-                                         (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0);
+                                         (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0, cols);
         if (e != cudaSuccess) return status_from(e);
         launches += 2;
         st = products(L, W, m, D, V, dH + (size_t)r0 * D, dW, p == 0, ws, s, &launches);
