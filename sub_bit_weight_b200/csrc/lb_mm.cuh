@@ -91,6 +91,8 @@ struct MmSmem {
 template <int kMaxProbs>
 constexpr size_t kMmSmemBytes = sizeof(MmSmem<kMaxProbs>) + 1024;
 
+static_assert(kMmSmemBytes<16> <= 232448, "the shared memory of one SM");
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");

@@ -48,7 +48,7 @@ namespace {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr int kMostMats = 64, kMostGroups = 8;   // of one set of launches
-constexpr int kNormBlocks = 128;                 // blocks (and partial sums) a matrix has at most
+constexpr int kNormBlocks = 592;                 // blocks (and partial sums) a matrix has at most
 constexpr int kSmallN = 64;
 constexpr float kSA = 8192.0f;                   // scale of A, q and A q
 constexpr int kMaxSteps = 10;
@@ -76,7 +76,10 @@ __device__ __forceinline__ float load_g(const void *G, size_t i, int bf16)
 // Partial sums of squares in binary64 (squares of float32 neither overflow nor vanish there).
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Mats P)
 {
-    const Mat &m = P.m[blockIdx.y];
+    pdl_go();
+    pdl_wait();
+    const int which = blockIdx.y;
+    const Mat &m = P.m[which];
     if ((int)blockIdx.x >= m.nblocks) return;
     const size_t n = (size_t)m.rows * m.cols;
     const size_t step = (size_t)m.nblocks * 256;
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ Mats 
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int i = 1; i < 8; ++i) s += w[i];
-        P.sums[blockIdx.y * kNormBlocks + blockIdx.x] = s;
+        P.sums[which * kNormBlocks + blockIdx.x] = s;
     }
 }
 
@@ -119,12 +122,16 @@ __device__ __forceinline__ void halves(float x, __half &hi, __half &lo)
 // X = G scaled to root mean square about 1, as binary16 halves.
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats P)
 {
-    const Mat &m = P.m[blockIdx.y];
+    pdl_go();
+    pdl_wait();
+    const int which = blockIdx.y;
+    const Mat &m = P.m[which];
     if ((int)blockIdx.x >= m.nblocks) return;
     __shared__ float sc;
     if (threadIdx.x < 32) {
         double s = 0.0;
-        for (int i = threadIdx.x; i < m.nblocks; i += 32) s += P.sums[blockIdx.y * kNormBlocks + i];
+#pragma unroll 4
+        for (int i = threadIdx.x; i < m.nblocks; i += 32) s += P.sums[which * kNormBlocks + i];
 #pragma unroll
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (threadIdx.x == 0) {
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats
             sc = (float)c;
             if (blockIdx.x == 0) {
                 const double kappa = 1.0 / (c * (norm + (double)P.eps));
-                P.scal[blockIdx.y] = norm == 0.0 ? make_float2(0.0f, 0.0f)
+                P.scal[which] = norm == 0.0 ? make_float2(0.0f, 0.0f)
                                                  : make_float2((float)kappa, (float)(kappa * kappa * kSA));
             }
         }
@@ -416,11 +423,11 @@ struct OrthEpi {
     }
 };
 
-// ---- A_0 from the Gram product's partial sums (tiles on and above the diagonal), n > 64: 32 x 32 blocks
+// ---- A_0 from the Gram product's partial sums (tiles on and above the diagonal)
 struct GroupArg {
     const float *part;    // [ranges][batch][n][pn]
     __half *A;            // [batch][2][n][pn]
-    int n, pn, ranges, batch, first, b0;   // b0: first block row of this group in the grid
+    int n, pn, ranges, batch, first, b0;   // b0: first matrix of this group in the grid
 };
 struct Groups {
     GroupArg g[kMostGroups];
@@ -428,57 +435,61 @@ struct Groups {
     const float2 *scal;
 };
 
-__device__ __forceinline__ float part_sum(const GroupArg &g, int b, int i, int j)
-{
-    if (i / kMmTile > j / kMmTile) {   // below the diagonal tiles: the mirrored element
-        const int t = i;
-        i = j;
-        j = t;
-    }
-    const size_t plane = (size_t)g.n * g.pn;
-    const float *p = g.part + (size_t)b * plane + (size_t)i * g.pn + j;
-    float s = 0.0f;
-    for (int r = 0; r < g.ranges; ++r) s += p[(size_t)r * g.batch * plane];
-    return s;
-}
-
+// n > 64: 64 x 64 blocks on and above the diagonal, written to both places
 __global__ void __launch_bounds__(256) gram_kernel(const __grid_constant__ Groups P)
 {
+    __shared__ float tile[64][65];
+    pdl_go();
+    pdl_wait();
     int q = 0;
     for (int i = 1; i < P.n; ++i)
         if ((int)blockIdx.y >= P.g[i].b0) q = i;
     const GroupArg &g = P.g[q];
-    const int b = blockIdx.y - g.b0, nb = (g.n + 31) / 32;
+    const int b = blockIdx.y - g.b0, nb = (g.n + 63) / 64;
     int ti = 0, t = blockIdx.x;
     if (t >= nb * (nb + 1) / 2) return;
     for (int left = nb; t >= left; --left, ++ti) t -= left;
     const int tj = ti + t;
     const float f = P.scal[g.first + b].y;
-    __shared__ float tile[32][33];
     const size_t plane = (size_t)g.n * g.pn;
     __half *A = g.A + (size_t)b * 2 * plane;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    for (int r = y; r < 32; r += 8) {
-        const int i = ti * 32 + r, j = tj * 32 + x;
-        const float s = i < g.n && j < g.n ? part_sum(g, b, i, j) * f : 0.0f;
-        tile[r][x] = s;
-        if (i < g.n && j < g.n) {
-            __half hi, lo;
-            halves(s, hi, lo);
-            A[(size_t)i * g.pn + j] = hi;
-            A[plane + (size_t)i * g.pn + j] = lo;
-        }
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;   // 4 columns; rows y, y + 16, ..
+    auto put = [&](int i, int j, const float (&v)[4]) {
+        alignas(8) __half hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) halves(v[k], hi[k], lo[k]);
+        *reinterpret_cast<uint2 *>(A + (size_t)i * g.pn + j) = *reinterpret_cast<uint2 *>(hi);
+        *reinterpret_cast<uint2 *>(A + plane + (size_t)i * g.pn + j) = *reinterpret_cast<uint2 *>(lo);
+    };
+    const int j = tj * 64 + 4 * x;
+    const float *part = g.part + (size_t)b * plane + (size_t)(ti * 64 + y) * g.pn + j;
+    const size_t step = (size_t)g.batch * plane;
+    float4 s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int r = 0; r < g.ranges; ++r)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (ti * 64 + y + 16 * k < g.n && j < g.pn) {
+                const float4 v = *reinterpret_cast<const float4 *>(part + r * step + (size_t)(16 * k) * g.pn);
+                s[k].x += v.x, s[k].y += v.y, s[k].z += v.z, s[k].w += v.w;
+            }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = ti * 64 + y + 16 * k;
+        const float v[4] = {s[k].x * f, s[k].y * f, s[k].z * f, s[k].w * f};
+        if (i < g.n && j < g.pn) put(i, j, v);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tile[y + 16 * k][4 * x + c] = v[c];
     }
     if (ti == tj) return;
     __syncthreads();
-    for (int r = y; r < 32; r += 8) {
-        const int i = tj * 32 + r, j = ti * 32 + x;
-        if (i < g.n && j < g.n) {
-            __half hi, lo;
-            halves(tile[x][r], hi, lo);
-            A[(size_t)i * g.pn + j] = hi;
-            A[plane + (size_t)i * g.pn + j] = lo;
-        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = tj * 64 + y + 16 * k, jj = ti * 64 + 4 * x;
+        const float v[4] = {tile[4 * x][y + 16 * k], tile[4 * x + 1][y + 16 * k], tile[4 * x + 2][y + 16 * k],
+                            tile[4 * x + 3][y + 16 * k]};
+        if (i < g.n && jj < g.pn) put(i, jj, v);
     }
 }
 
@@ -585,19 +596,26 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
 {
     extern __shared__ __align__(16) float sm[];
     float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP;
+    pdl_go();
+    pdl_wait();
     int w = 0;
     for (int i = 1; i < P.n; ++i)
         if ((int)blockIdx.x >= P.g[i].b0) w = i;
     const GroupArg &g = P.g[w];
     const int b = blockIdx.x - g.b0, n = g.n;
     const float f = P.scal[g.first + b].y * (1.0f / kSA);
+    const size_t plane = (size_t)n * g.pn;
     for (int e = threadIdx.x; e < 64 * 64; e += 256) {
         const int i = e >> 6, j = e & 63;
-        A[i * kSmallP + j] = i < n && j < n ? part_sum(g, b, i, j) * f : 0.0f;
+        float a = 0.0f;
+        if (i < n && j < n) {
+            const float *p = g.part + (size_t)b * plane + (size_t)i * g.pn + j;
+            for (int r = 0; r < g.ranges; ++r) a += p[(size_t)r * g.batch * plane];
+        }
+        A[i * kSmallP + j] = a * f;
     }
     __syncthreads();
     small_chain(A, p, T, Q, n, steps);
-    const size_t plane = (size_t)n * g.pn;
     __half *D = g.A + (size_t)b * 2 * plane;
     for (int e = threadIdx.x; e < 64 * 64; e += 256) {
         const int i = e >> 6, j = e & 63;
@@ -776,8 +794,8 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
                 g.wide = rows[i] < cols[i];
                 g.m = std::max(rows[i], cols[i]);
                 g.n = std::min(rows[i], cols[i]);
-                g.pn = (g.n + 7) & ~7;
-                g.pitch = (cols[i] + 7) & ~7;
+                g.pn = (g.n + 63) & ~63;
+                g.pitch = (cols[i] + 63) & ~63;
                 g.first = (int)C.order.size();
                 C.groups.push_back(g);
             }
@@ -789,14 +807,33 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             out.push_back(std::move(C));
             continue;
         }
-        // ranges of the Gram products: units of about a quarter of a pair's share, at least 24 k blocks (6 us)
-        const int parts = bf16 ? 1 : 3;
+        // Ranges of the Gram products.  In k blocks of a pair (0.27 us): the longest list of units as they are dealt, and
+        // the writing and reading of the ranges' partial sums at the copy rate.  Units of at least 24 k blocks.
+        const int parts = bf16 ? 1 : 3, pairs = 74;
         double total = 0.0;
-        for (const Group &g : C.groups) {
-            const double nt = (g.n + kMmTile - 1) / kMmTile;
-            total += nt * (nt + 1) / 2 * g.batch * parts * ((g.m + kMmBK - 1) / kMmBK);
+        for (const Group &g : C.groups)
+            total += (double)mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + kMmTile - 1) / kMmTile, true, kMmTile) * g.batch *
+                     parts * ((g.m + kMmBK - 1) / kMmBK);
+        long unit = 24;
+        double best = 1e300;
+        for (int c = 1; c <= 12; ++c) {
+            const long u = std::max(24L, (long)(total / (pairs * c)) + 1);
+            std::vector<double> load(pairs, 0.0);
+            double bytes = 0.0;
+            long at_unit = 0;
+            for (const Group &g : C.groups) {
+                const long k = (long)parts * ((g.m + kMmBK - 1) / kMmBK), r = std::min(64L, (k + u - 1) / u), per = (k + r - 1) / r;
+                const long tiles = mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + kMmTile - 1) / kMmTile, true, kMmTile);
+                for (long x = 0; x < tiles * g.batch * r; ++x) load[at_unit++ % pairs] += (double)per + 4.0;
+                bytes += (double)r * g.batch * g.n * g.pn * 4.0 * 2.0;
+            }
+            const double cost = *std::max_element(load.begin(), load.end()) + bytes / 1.8e6;
+            if (cost < best) {
+                best = cost;
+                unit = u;
+            }
+            if (u == 24) break;
         }
-        const long unit = std::max(24L, (long)(total / (74 * 4)));
         size_t o = 0;
         auto take = [&](size_t b) {
             const size_t r = o;
@@ -850,8 +887,10 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
             m.nblocks = (int)std::min<size_t>(kNormBlocks, (n + 8191) / 8192);
             most_blocks = std::max(most_blocks, m.nblocks);
         }
-    norm_kernel<<<dim3(most_blocks, M.n), 256, 0, s>>>(M);
-    split_kernel<<<dim3(most_blocks, M.n), 256, 0, s>>>(M);
+    const dim3 blocks_of_all(most_blocks, M.n);
+    cudaError_t e = launch_after(norm_kernel, blocks_of_all, 256, s, M);
+    if (e != cudaSuccess) return status_from(e);
+    if ((e = launch_after(split_kernel, blocks_of_all, 256, s, M)) != cudaSuccess) return status_from(e);
     *launches += 2;
 
     MmBatch<kMostProbs> B;
@@ -861,8 +900,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     for (int i = 0; i < M.n; ++i) E.out[i] = Os[C.order[i]];
     const int parts = bf16 ? 1 : 3, xz = bf16 ? 1 : 2;
     int pairs = 0;
-    cudaError_t e = mm_pairs(&pairs);
-    if (e != cudaSuccess) return status_from(e);
+    if ((e = mm_pairs(&pairs)) != cudaSuccess) return status_from(e);
     // Widest tiles of a launch that still give every pair of SMs one: a few small matrices are bound by the length of one
     // tile's chain (copy, products, epilogue), many or large ones by the operands read per tile.
     auto width_of = [&](auto &&tiles) {
@@ -930,11 +968,11 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         a.first = g.first;
         a.b0 = sm ? smalls : bigs;
         (sm ? smalls : bigs) += g.batch;
-        const int nb = (g.n + 31) / 32;
+        const int nb = (g.n + 63) / 64;
         if (!sm) blocks = std::max(blocks, nb * (nb + 1) / 2);
     }
     if (bigs) {
-        gram_kernel<<<dim3(blocks, bigs), 256, 0, s>>>(big);
+        if ((e = launch_after(gram_kernel, dim3(blocks, bigs), 256, s, big)) != cudaSuccess) return status_from(e);
         ++*launches;
     }
     if (smalls) {

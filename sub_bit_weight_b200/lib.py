@@ -519,6 +519,17 @@ _sig("lb_train_status", _st, [_vp])
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
+_ARRAYS: dict = {}
+
+
+def _array(ctype, n: int):
+    """The ctypes array type of n elements (making one anew takes as long as the rest of a small call's marshalling)."""
+    t = _ARRAYS.get((ctype, n))
+    if t is None:
+        t = _ARRAYS[ctype, n] = ctype * n
+    return t
+
+
 class _Names:
     """Names of the entries of a list argument, made only where an error asks for one."""
 
@@ -698,13 +709,13 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
             raise ValueError(f"G[{i}] must be a matrix with at least one element")
     dtype, names = G[0].dtype, _Names("G")
     code = _element(dtype, "G")
-    rows, cols = (_i * n)(*[r for r, _ in shapes]), (_i * n)(*[c for _, c in shapes])
+    ints, ptrs = _array(_i, n), _array(_vp, n)
+    rows, cols = ints(*[r for r, _ in shapes]), ints(*[c for _, c in shapes])
     with _On(stream, G, names) as on:
-        src = (_vp * n)(*[t.data_ptr() if t.dtype is dtype and t.is_contiguous() else _dev(t, dtype, names[i])
-                          for i, t in enumerate(G)])
+        src = ptrs(*[t.data_ptr() if t.dtype is dtype and t.is_contiguous() else _dev(t, dtype, names[i])
+                     for i, t in enumerate(G)])
         out = [torch.empty(shape, dtype=torch.bfloat16, device=on.device) for shape in shapes]
         ws = _workspace(workspace, int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code)), on)
-        _check(_lib.lb_orthogonalise(src, code, rows, cols, n, int(steps), float(eps),
-                                     (_vp * n)(*[t.data_ptr() for t in out]), _dev(ws, torch.uint8, "workspace"),
-                                     ws.numel(), on.stream), "lb_orthogonalise")
+        _check(_lib.lb_orthogonalise(src, code, rows, cols, n, int(steps), float(eps), ptrs(*[t.data_ptr() for t in out]),
+                                     _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream), "lb_orthogonalise")
     return out
