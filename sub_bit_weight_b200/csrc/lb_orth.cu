@@ -493,109 +493,78 @@ __global__ void __launch_bounds__(256) gram_kernel(const __grid_constant__ Group
     }
 }
 
-// ---- n <= 64: the whole polynomial in one block, float32
-constexpr int kSmallP = 68;   // row pitch of the shared matrices
-// C = X Y for symmetric X (row k of X serves as its column k); thread (ty, tx) holds C[4 ty ..][4 tx ..]
-__device__ __forceinline__ void small_mul(const float *X, const float *Y, int n, int ty, int tx, float (&c)[4][4])
+// ---- n <= 64: the whole polynomial in one block of 1024 threads, float32
+// Thread (ty, tx) has the elements (ty + 32 a, tx + 32 b) on and above the diagonal, and writes each to both its places (see
+// OrthEpi).  A row's threads read one word of X together and 32 words of Y side by side; a pitch of 65 spreads the columns
+// that the mirror images go to over all banks.
+constexpr int kSmallP = 65;
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallMat = 64 * kSmallP;
+
+// c = s X Y + t D for symmetric X (its row k serves as its column k)
+__device__ __forceinline__ void small_mul(const float *X, const float *Y, const float *D, float s, float t, int n,
+                                          float (&c)[2][2])
 {
+    const int ty = threadIdx.x >> 5, tx = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-    // four rows at a time (rows n .. are zero), so that their reads overlap
-    for (int k = 0; k < n; k += 4) {
-        float4 x[4], y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            x[u] = *reinterpret_cast<const float4 *>(X + (k + u) * kSmallP + 4 * ty);
-            y[u] = *reinterpret_cast<const float4 *>(Y + (k + u) * kSmallP + 4 * tx);
+        for (int b = a; b < 2; ++b) {
+            const int i = ty + 32 * a, j = tx + 32 * b;
+            if (i >= n || j >= n || i > j) continue;
+            float u = 0.0f, v = 0.0f;
+            int k = 0;
+#pragma unroll 4
+            for (; k + 1 < n; k += 2) {
+                u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
+                v = fmaf(X[(k + 1) * kSmallP + i], Y[(k + 1) * kSmallP + j], v);
+            }
+            if (k < n) u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
+            c[a][b] = fmaf(s, u + v, t * D[i * kSmallP + j]);
         }
+}
+
+__device__ __forceinline__ void small_put(float *D, int n, const float (&c)[2][2], float diagonal = 0.0f)
+{
+    const int ty = threadIdx.x >> 5, tx = threadIdx.x & 31;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
+        for (int b = a; b < 2; ++b) {
+            const int i = ty + 32 * a, j = tx + 32 * b;
+            if (i >= n || j >= n || i > j) continue;
+            D[i * kSmallP + j] = D[j * kSmallP + i] = c[a][b] + (i == j ? diagonal : 0.0f);
         }
-    }
 }
 
-// blocks on and above the diagonal, written to both places (see OrthEpi)
-__device__ __forceinline__ void small_put(float *D, int ty, int tx, const float (&c)[4][4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (4 * ty + i <= 4 * tx + j)
-                D[(4 * ty + i) * kSmallP + 4 * tx + j] = D[(4 * tx + j) * kSmallP + 4 * ty + i] = c[i][j];
-}
-
-// c = a D + c
-__device__ __forceinline__ void small_add(const float *D, int ty, int tx, float a, float (&c)[4][4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(a, D[(4 * ty + i) * kSmallP + 4 * tx + j], c[i][j]);
-}
-
-// Q_steps from A (both 64 x kSmallP in shared memory; p and T are scratch); at least 256 threads,
-// ends synchronised
+// Q_steps from A (shared memory, kSmallMat floats each; p and T are scratch); ends synchronised
 __device__ __forceinline__ void small_chain(float *A, float *p, float *T, float *Q, int n, int steps)
 {
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const bool mine = ty <= tx && 4 * tx < n;
-    float c[4][4];
+    float c[2][2], d[2][2];
     for (int k = 0; k < steps; ++k) {
-        if (mine) {
-            small_mul(A, A, n, ty, tx, c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) c[i][j] *= kC;
-            small_add(A, ty, tx, kB, c);
-            small_put(p, ty, tx, c);
-            if (k == 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (4 * ty + i == 4 * tx + j) c[i][j] += kA;
-                small_put(Q, ty, tx, c);
-            }
+        small_mul(A, A, A, kC, kB, n, c);
+        small_put(p, n, c);
+        if (k == 0) small_put(Q, n, c, kA);
+        __syncthreads();
+        if (k > 0) small_mul(Q, p, Q, 1.0f, kA, n, d);
+        if (k + 1 < steps) {
+            small_mul(A, p, A, 1.0f, kA, n, c);
+            small_put(T, n, c);
         }
         __syncthreads();
-        if (k > 0) {
-            if (mine) {
-                small_mul(Q, p, n, ty, tx, c);
-                small_add(Q, ty, tx, kA, c);
-            }
-            __syncthreads();
-            if (mine) small_put(Q, ty, tx, c);
-        }
+        if (k > 0) small_put(Q, n, d);
         if (k + 1 < steps) {
-            if (mine) {
-                small_mul(A, p, n, ty, tx, c);
-                small_add(A, ty, tx, kA, c);
-                small_put(T, ty, tx, c);
-            }
-            __syncthreads();
-            if (mine) {
-                small_mul(T, p, n, ty, tx, c);
-                small_add(T, ty, tx, kA, c);
-                small_put(A, ty, tx, c);
-            }
+            small_mul(T, p, T, 1.0f, kA, n, c);
+            small_put(A, n, c);
         }
         __syncthreads();
     }
 }
 
-__global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
 {
     extern __shared__ __align__(16) float sm[];
-    float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP;
+    float *A = sm, *p = A + kSmallMat, *T = p + kSmallMat, *Q = T + kSmallMat;
     pdl_go();
     pdl_wait();
     int w = 0;
@@ -605,19 +574,19 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
     const int b = blockIdx.x - g.b0, n = g.n;
     const float f = P.scal[g.first + b].y * (1.0f / kSA);
     const size_t plane = (size_t)n * g.pn;
-    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+    for (int e = threadIdx.x; e < 64 * 64; e += kSmallThreads) {
         const int i = e >> 6, j = e & 63;
+        if (i >= n || j >= n) continue;
+        const float *part = g.part + (size_t)b * plane + (size_t)i * g.pn + j;
         float a = 0.0f;
-        if (i < n && j < n) {
-            const float *p = g.part + (size_t)b * plane + (size_t)i * g.pn + j;
-            for (int r = 0; r < g.ranges; ++r) a += p[(size_t)r * g.batch * plane];
-        }
+#pragma unroll 4
+        for (int r = 0; r < g.ranges; ++r) a += part[(size_t)r * g.batch * plane];
         A[i * kSmallP + j] = a * f;
     }
     __syncthreads();
     small_chain(A, p, T, Q, n, steps);
     __half *D = g.A + (size_t)b * 2 * plane;
-    for (int e = threadIdx.x; e < 64 * 64; e += 256) {
+    for (int e = threadIdx.x; e < 64 * 64; e += kSmallThreads) {
         const int i = e >> 6, j = e & 63;
         if (i < n && j < n) {
             __half hi, lo;
@@ -630,7 +599,6 @@ __global__ void __launch_bounds__(256) small_kernel(const __grid_constant__ Grou
 
 // ---- a whole small matrix in one block
 constexpr int kTinyElems = 24576;   // m times n rounded up to 4
-constexpr int kTinyThreads = 1024;
 struct TinyMat {
     const void *G;
     uint16_t *O;
@@ -642,48 +610,59 @@ struct Tinies {
     float eps;
 };
 
-__global__ void __launch_bounds__(kTinyThreads) tiny_kernel(const __grid_constant__ Tinies P)
+__global__ void __launch_bounds__(kSmallThreads) tiny_kernel(const __grid_constant__ Tinies P)
 {
     extern __shared__ __align__(16) float sm[];
-    float *A = sm, *p = A + 64 * kSmallP, *T = p + 64 * kSmallP, *Q = T + 64 * kSmallP, *X = Q + 64 * kSmallP;
-    __shared__ double sums[32];
+    float *X = sm;                                        // m x pitch: G, or its transpose
+    __shared__ double sums[32], scale;
     const TinyMat &M = P.m[blockIdx.x];
     const int rows = M.rows, cols = M.cols, tid = threadIdx.x;
     const bool wide = rows < cols;
-    const int m = max(rows, cols), n = min(rows, cols), pitch = (n + 3) & ~3;   // X is m x n: G, or its transpose
-    const int total = rows * cols;
+    const int m = max(rows, cols), n = min(rows, cols), pitch = (n + 3) & ~3;
+    const int total = rows * cols, size = m * pitch;
+    float *A = X + size, *p = A + kSmallMat, *T = p + kSmallMat, *Q = T + kSmallMat;
 
+    if (pitch != n)
+        for (int e = tid; e < size; e += kSmallThreads) X[e] = 0.0f;
+    if (pitch != n) __syncthreads();
     double s = 0.0;
-    for (int e = tid; e < m * pitch; e += kTinyThreads)
-        if (e % pitch >= n) X[e] = 0.0f;
+    const float inv = 1.0f / (float)cols;   // total < 2^15: the quotient below is exact
 #pragma unroll 8
-    for (int e = tid; e < total; e += kTinyThreads) {
+    for (int e = tid; e < total; e += kSmallThreads) {
         const float x = load_g(M.G, e, P.bf16);
-        const int r = e / cols, c = e - r * cols;
+        const int r = (int)(((float)e + 0.5f) * inv), c = e - r * cols;
         X[wide ? c * pitch + r : r * pitch + c] = x;
         s += (double)x * x;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((tid & 31) == 0) sums[tid >> 5] = s;
-    for (int e = tid; e < 64 * kSmallP; e += kTinyThreads) A[e] = 0.0f;
     __syncthreads();
-    s = 0.0;
-    for (int i = 0; i < kTinyThreads / 32; ++i) s += sums[i];
-    const double norm = sqrt(s), f = norm == 0.0 ? 0.0 : 1.0 / (norm + (double)P.eps);
-    for (int e = tid; e < m * pitch; e += kTinyThreads) X[e] = (float)(X[e] * f);
+    if (tid < 32) {
+        s = sums[tid];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (tid == 0) {
+            const double norm = sqrt(s);
+            scale = norm == 0.0 ? 0.0 : 1.0 / (norm + (double)P.eps);
+        }
+    }
+    __syncthreads();
+    const double f = scale;
+    for (int e = tid; e < size; e += kSmallThreads) X[e] = (float)(X[e] * f);
     __syncthreads();
 
     // A = X^T X: 4 x 4 tiles, the rows of X dealt to as many groups of threads as there are
     {
-        const int td = pitch / 4, tiles = td * td, groups = min(kTinyThreads / tiles, 3 * 64 * kSmallP / (pitch * pitch));
+        const int td = pitch / 4, tiles = td * td, groups = min(kSmallThreads / tiles, 3 * kSmallMat / (pitch * pitch));
         const int g = tid / tiles, t = tid - g * tiles, ty = t / td, tx = t - ty * td;
-        float c[4][4];
+        float *const part = p;   // the groups' sums in p, T and Q, which are one array, then added in order
+        if (g < groups) {
+            float c[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
-        if (g < groups)
+                for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
 #pragma unroll 4
             for (int k = g; k < m; k += groups) {
                 const float4 x = *reinterpret_cast<const float4 *>(X + k * pitch + 4 * ty);
@@ -694,17 +673,15 @@ __global__ void __launch_bounds__(kTinyThreads) tiny_kernel(const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
             }
-        // the groups' sums in p, T and Q, which are one array, then added in order
-        float *const part = p;
-        if (g < groups)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4 *>(part + (g * pitch + 4 * ty + i) * pitch + 4 * tx) =
-                    make_float4(c[i][0], c[i][1], c[i][2], c[i][3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part[(g * pitch + 4 * ty + i) * pitch + 4 * tx + j] = c[i][j];
+        }
         __syncthreads();
-        for (int e = tid; e < pitch * pitch; e += kTinyThreads) {
+        for (int e = tid; e < pitch * pitch; e += kSmallThreads) {
             float a = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < groups; ++i) a += part[i * pitch * pitch + e];
             A[e / pitch * kSmallP + e % pitch] = a;
         }
@@ -712,27 +689,41 @@ __global__ void __launch_bounds__(kTinyThreads) tiny_kernel(const __grid_constan
     }
     small_chain(A, p, T, Q, n, P.steps);
 
-    // the update, 4 columns of a row of X Q at a time
-    for (int e = tid; e < m * (pitch / 4); e += kTinyThreads) {
-        const int i = e % m, j = e / m * 4;
+    // Q with rows of 64, for reads of 4 columns at once (into A and p, which are done with)
+    float *const Q4 = reinterpret_cast<float *>(((uintptr_t)A + 15) & ~(uintptr_t)15);
+    for (int e = tid; e < n * 64; e += kSmallThreads) Q4[e] = (e & 63) < n ? Q[(e >> 6) * kSmallP + (e & 63)] : 0.0f;
+    for (int e = n * 64 + tid; e < pitch * 64; e += kSmallThreads) Q4[e] = 0.0f;
+    __syncthreads();
+    // the update, 4 columns of a row of X Q at a time; neighbours take the other columns of the row
+    const int nj = pitch / 4;
+    const float inv_nj = 1.0f / (float)nj;
+    const bool vec = !wide && n % 4 == 0 && ((uintptr_t)M.O & 7) == 0;
+    for (int e = tid; e < m * nj; e += kSmallThreads) {
+        const int i = (int)(((float)e + 0.5f) * inv_nj), j = 4 * (e - i * nj);
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float x = X[i * pitch + k];
-            const float4 q = *reinterpret_cast<const float4 *>(Q + k * kSmallP + j);
-            a.x = fmaf(x, q.x, a.x);
-            a.y = fmaf(x, q.y, a.y);
-            a.z = fmaf(x, q.z, a.z);
-            a.w = fmaf(x, q.w, a.w);
-        }
-        const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll 2
+        for (int k = 0; k < pitch; k += 4) {
+            const float4 x4 = *reinterpret_cast<const float4 *>(X + i * pitch + k);
+            const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (j + u < n) {
-                uint16_t o;
-                asm("cvt.rn.bf16.f32 %0, %1;\n" : "=h"(o) : "f"(v[u]));
-                M.O[wide ? (size_t)(j + u) * m + i : (size_t)i * n + j + u] = o;
+            for (int u = 0; u < 4; ++u) {
+                const float4 q = *reinterpret_cast<const float4 *>(Q4 + (k + u) * 64 + j);
+                a.x = fmaf(x[u], q.x, a.x);
+                a.y = fmaf(x[u], q.y, a.y);
+                a.z = fmaf(x[u], q.z, a.z);
+                a.w = fmaf(x[u], q.w, a.w);
             }
+        }
+        const uint32_t lo = pack_bf(__float_as_uint(a.x), __float_as_uint(a.y), 1.0f);
+        const uint32_t hi = pack_bf(__float_as_uint(a.z), __float_as_uint(a.w), 1.0f);
+        if (vec) {
+            *reinterpret_cast<uint2 *>(M.O + (size_t)i * n + j) = make_uint2(lo, hi);
+        } else {
+            const uint16_t o[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (j + u < n) M.O[wide ? (size_t)(j + u) * m + i : (size_t)i * n + j + u] = o[u];
+        }
     }
 }
 
@@ -976,9 +967,9 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         ++*launches;
     }
     if (smalls) {
-        const size_t smem = 4 * 64 * kSmallP * sizeof(float);
+        const size_t smem = 4 * kSmallMat * sizeof(float);
         if ((e = ensure_dyn_smem((const void *)small_kernel, smem)) != cudaSuccess) return status_from(e);
-        small_kernel<<<smalls, 256, smem, s>>>(small, steps, q_scale_after(steps));
+        small_kernel<<<smalls, kSmallThreads, smem, s>>>(small, steps, q_scale_after(steps));
         ++*launches;
     }
 
@@ -1079,10 +1070,10 @@ lb_status tiny_chunk(const Chunk &C, const void *const *Gs, const int *rows, con
         T.m[k] = TinyMat{Gs[i], Os[i], rows[i], cols[i]};
         most = std::max(most, m * ((n + 3) & ~3));
     }
-    const size_t smem = (size_t)(4 * 64 * kSmallP + most) * sizeof(float);
+    const size_t smem = (size_t)(4 * kSmallMat + most) * sizeof(float);
     const cudaError_t e = ensure_dyn_smem((const void *)tiny_kernel, smem);
     if (e != cudaSuccess) return status_from(e);
-    tiny_kernel<<<(unsigned)C.order.size(), kTinyThreads, smem, s>>>(T);
+    tiny_kernel<<<(unsigned)C.order.size(), kSmallThreads, smem, s>>>(T);
     ++*launches;
     return status_from(cudaGetLastError());
 }
