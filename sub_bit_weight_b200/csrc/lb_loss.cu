@@ -489,8 +489,8 @@ int dh_splits(int M, int D, int V, bool with_dW, int pairs)
 
 // A forward pass of at most 128 rows is bound by reading W.  With the rows as the 256-wide side of the tiles the tensor
 // cores multiply mostly zeros, and take longer than the reading (118 us at M = 16, D = 8192, V = 32000); so W is that
-// side, and the rows are the columns (as few as 32).  Its tiles (256 vocabulary entries) divide badly, 125 on 74 pairs take
-// as long as 148, which cutting k into ranges evens out; the ranges' logits have to be written, read and added.
+// side, and the rows are the columns (as few as 32): 101 us.  Its tiles (256 vocabulary entries) divide badly, 125 on 74
+// pairs take as long as 148, which cutting k into ranges evens out; the ranges' logits have to be written, read and added.
 // In bytes a pair waits for: the longest list of units, and its share of the logits.
 int few_ranges(int M, int D, int V)
 {
@@ -499,7 +499,8 @@ int few_ranges(int M, int D, int V)
     long best = 1;
     double best_cost = 0.0;
     for (long s = 1; s <= 16 && s <= nkb; ++s) {
-        const double rounds = (double)((tiles * s + pairs - 1) / pairs), unit = (double)((nkb + s - 1) / s) * kMmBK * kMmTile * 2;
+        const double rounds = (double)((tiles * s + pairs - 1) / pairs);
+        const double unit = (double)((nkb + s - 1) / s) * kMmBK * kMmTile * 2;
         const double cost = rounds * unit + (double)s * M * V * 8 / pairs;
         if (s == 1 || cost < 0.98 * best_cost) {
             best_cost = cost;
@@ -670,8 +671,8 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     if (P.splits > 1) {
         const size_t nvec = (size_t)M * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
-        const cudaError_t r = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.part), (size_t)tile_rows * D / 4, P.splits, nvec,
-                                              E.wref, (uint4 *)dH);
+        const cudaError_t r = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.part),
+                                           (size_t)tile_rows * D / 4, P.splits, nvec, E.wref, (uint4 *)dH);
         if (r != cudaSuccess) return status_from(r);
         ++*launches;
     }
@@ -778,8 +779,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     if (dW && L.npieces > 1) {
         const size_t nvec = (size_t)V * D / 8;
         const int grid = (int)std::min<size_t>((nvec + 255) / 256, 148 * 8);
-        const cudaError_t e = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.acc), 0, 1, nvec, (const float *)(ws + L.wref),
-                                              (uint4 *)dW);
+        const cudaError_t e = launch_after(round_sum_kernel, dim3(grid), 256, s, (const float4 *)(ws + L.acc), 0, 1, nvec,
+                                           (const float *)(ws + L.wref), (uint4 *)dW);
         if (e != cudaSuccess) return status_from(e);
         ++launches;
     }

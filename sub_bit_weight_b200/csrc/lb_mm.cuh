@@ -13,13 +13,25 @@
 // L2 is what paces such a kernel.  A problem with few tiles takes them 128 or
 // 64 columns wide.
 //
-// Roles (12 warps a CTA): one thread each of warps 0 and 2 issues the TMA
-// copies of its CTA's half of A and of B; warp 1 of the pair's first CTA one thread issues the MMAs for both;
-// warps 4-11 the epilogue (128 rows of the CTA, one thread a row and half of
-// the columns; an epilogue that holds its columns in registers takes registers
-// over from warps 0-3).  Two accumulators of 256 columns let the epilogue of one unit
-// overlap the main loop of the next.  Units (tile, or a k range of a tile) are
-// dealt to the pairs in order; a launch may hold several problems.
+// Roles (12 warps a CTA): warps 0 and 2 issue the TMA copies of their CTA's
+// half of A and of B; warp 1 of the pair's first CTA issues the MMAs for both;
+// warps 4-11 are the epilogue (128 rows of the CTA, one thread a row and half
+// of the columns; an epilogue that holds its columns in registers takes
+// registers over from warps 0-3).  Two accumulators of 256 columns let the
+// epilogue of one unit overlap the main loop of the next.  Units (tile, or a k
+// range of a tile) are dealt to the pairs in order; a launch may hold several
+// problems.
+//
+// What bounds it: 64 k of a 256 x 256 tile are 512 cycles of the tensor cores,
+// and the 32 KB a CTA copies for them are 64 bytes a cycle, about what an SM
+// gets from L2.  Measured (cycles for 64 k, where a logit GEMM of 2048 x 32000
+// x 5120 runs): 786 with one thread for both copies and loop state in shared
+// memory, 614 with two threads and registers, 513 with the issuing warps
+// converged, so that descriptors stay in uniform registers; that is 1.36 PFLOP/s,
+// the clock held down by power.  What adds requests to L2 beside the copies
+// costs time at once: prefetches a unit ahead (+27 %), an epilogue whose lanes
+// walk a row each (+35 % in the n x n products of lb_orth.cu), and operand rows
+// that do not begin on 128 bytes (+30 % with rows of 2320 bytes).
 //
 // The tensor core adds to its accumulator with truncation (measured: 16 terms
 // at a time, about 1.5 * 2^-24 of the accumulator lost on average, toward
@@ -284,7 +296,8 @@ struct MmTileCtx {
 
 // An epilogue `Epi` is called by each of its warps, for each unit: begin() (before the accumulator is there), take() for
 // each chunk (`first`, `last`) while the accumulator is held, end() after it has been released.  `State` lives from
-// begin() to end(); kManyRegs asks for the register split; `stored` says whether the staging block has copies that may still be reading it.
+// begin() to end(); kManyRegs asks for the register split; `stored` says whether the staging block has copies that may
+// still be reading it.
 template <bool kBf16, int kMaxProbs, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     mm_kernel(const __grid_constant__ MmBatch<kMaxProbs> G, const __grid_constant__ typename Epi::Params E)
@@ -333,59 +346,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 
     if (warp < 4) {
         if constexpr (Epi::kManyRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kMmRegsFew));
-        // What the loops below use of a problem is in registers before they start: one of these threads has about 500
-        // cycles for a k block, and a shared-memory read is 30 of them.
+        // What the loops below use of a problem is in registers before they start: a k block takes about 500 cycles, and a
+        // shared-memory read is 30 of them.
         if (warp == 0 || warp == 2) {
             // ---------------- producers: warp 0 copies A, warp 2 B
-            {
-                const bool is_a = warp == 0;
-                unsigned char *const base = is_a ? S.A[0] : S.B[0];
-                const uint32_t full0 = map_rank(smem_u32(&S.full[0]), 0);
-                uint32_t s = 0, ph = 0;
-                bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 ; ++n) {
-                    const MmUnit U = mm_unit(S.p, nprobs, u);
-                    const MmProb &P = S.p[U.q];
-                    const CUtensorMap *const map = is_a ? &G.mA[U.q] : &G.mB[U.q];
-                    const bool mn = is_a ? P.a_mn != 0 : P.b_mn != 0;
-                    const bool two = mn && (is_a || U.half > 64);   // both 64-wide slices
-                    const int x0 = is_a ? U.tm * kMmTile + (int)rank * kMmHalf : U.tn * P.width + (int)rank * U.half;
-                    // both CTAs' halves of both operands; a K-major box of B has width / 2 rows
-                    const uint32_t bytes =
-                        2 * (kMmOperand + (P.b_mn ? (U.half > 64 ? 2 : 1) * kMmSlice : P.width * kMmBK));
-                    const int nkb = P.nkb, parts = P.parts, z0 = U.b * (is_a ? P.za : P.zb);
-                    // low halves first (the accumulator truncates by what is already in it): with three parts
-                    // lo * hi, hi * lo, hi * hi; with two the operand that has a low half
-                    const int low = parts == 3 ? (is_a ? 0 : 1) : parts == 2 && (is_a == (P.b_whole != 0)) ? 0 : -1;
-                    int seg = U.kb0 / nkb, kb = U.kb0 - seg * nkb;
-                    for (int left = U.kb1 - U.kb0; left > 0; --left) {
-                        if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
-                        const bool one = elect_one();
-                        if (one && is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
-                        unsigned char *const dst = base + s * kMmOperand;
-                        const uint32_t bar = full0 + s * 8;
-                        const int k = kb * kMmBK, z = z0 + (seg == low ? 1 : 0);
-                        if (one) {
-                            tma_load_3d_pair(dst, map, mn ? x0 : k, mn ? k : x0, z, bar);
-                            if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z, bar);
-                        }
-                        __syncwarp();
-                        if (++kb == nkb) {
-                            kb = 0;
-                            ++seg;
-                        }
-                        if (++s == kMmStages) {
-                            s = 0;
-                            ph ^= 1;
-                        }
+            const bool is_a = warp == 0;
+            unsigned char *const base = is_a ? S.A[0] : S.B[0];
+            const uint32_t full0 = map_rank(smem_u32(&S.full[0]), 0);
+            uint32_t s = 0, ph = 0;
+            bool ok = true;
+            for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0; ++n) {
+                const MmUnit U = mm_unit(S.p, nprobs, u);
+                const MmProb &P = S.p[U.q];
+                const CUtensorMap *const map = is_a ? &G.mA[U.q] : &G.mB[U.q];
+                const bool mn = is_a ? P.a_mn != 0 : P.b_mn != 0;
+                const bool two = mn && (is_a || U.half > 64);   // both 64-wide slices
+                const int x0 = is_a ? U.tm * kMmTile + (int)rank * kMmHalf : U.tn * P.width + (int)rank * U.half;
+                // both CTAs' halves of both operands; a K-major box of B has width / 2 rows
+                const uint32_t bytes =
+                    2 * (kMmOperand + (P.b_mn ? (U.half > 64 ? 2 : 1) * kMmSlice : P.width * kMmBK));
+                const int nkb = P.nkb, parts = P.parts, z0 = U.b * (is_a ? P.za : P.zb);
+                // low halves first (the accumulator truncates by what is already in it): with three parts
+                // lo * hi, hi * lo, hi * hi; with two the operand that has a low half
+                const int low = parts == 3 ? (is_a ? 0 : 1) : parts == 2 && (is_a == (P.b_whole != 0)) ? 0 : -1;
+                int seg = U.kb0 / nkb, kb = U.kb0 - seg * nkb;
+                for (int left = U.kb1 - U.kb0; left > 0; --left) {
+                    if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
+                    const bool one = elect_one();
+                    if (one && is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
+                    unsigned char *const dst = base + s * kMmOperand;
+                    const uint32_t bar = full0 + s * 8;
+                    const int k = kb * kMmBK, z = z0 + (seg == low ? 1 : 0);
+                    if (one) {
+                        tma_load_3d_pair(dst, map, mn ? x0 : k, mn ? k : x0, z, bar);
+                        if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z, bar);
+                    }
+                    __syncwarp();
+                    if (++kb == nkb) {
+                        kb = 0;
+                        ++seg;
+                    }
+                    if (++s == kMmStages) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
-                if (*abort) {
-                    // let the copies already issued land before the pair leaves: a wait gives up after two seconds, a copy
-                    // takes microseconds, so a fixed time is enough
-                    const long long t0 = clock64();
-                    while (clock64() - t0 < kWaitCycles / 1000) {
-                    }
+            }
+            if (*abort) {
+                // let the copies already issued land before the pair leaves: a wait gives up after two seconds, a copy
+                // takes microseconds, so a fixed time is enough
+                const long long t0 = clock64();
+                while (clock64() - t0 < kWaitCycles / 1000) {
                 }
             }
         } else if (warp == 1) {
@@ -393,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             if (rank == 0) {
                 uint32_t s = 0, ph = 0, acc = 0;   // stage, its phase, accumulators used
                 bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 ; ++n) {
+                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0; ++n) {
                     const MmUnit U = mm_unit(S.p, nprobs, u);
                     const MmProb &P = S.p[U.q];
                     const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;

@@ -9,7 +9,7 @@
 // is X_0 times a polynomial of A_0 = X_0^T X_0, so the long axis is needed
 // twice only, and everything between is n x n:
 //
-//     q_k = a I + b A_k + c A_k^2,   A_{k+1} = A_k q_k^2,   Q_{k+1} = Q_k q_k,   X_steps = X_0 Q_steps
+//     p_k = b A_k + c A_k^2,  q_k = a I + p_k,   A_{k+1} = A_k q_k^2,   Q_{k+1} = Q_k q_k,   X_steps = X_0 Q_steps
 //
 // 2 m n^2 (half of it by symmetry) + 2 m n^2 + steps * 4 * 2 n^3 flops instead
 // of steps * (4 m n^2 + 2 n^3).  All these n x n matrices are polynomials of
@@ -20,20 +20,31 @@
 // blows up (by up to a^steps = 485), and in A_0 they are squared, so an error
 // of 2^-12 in A (one binary16 rounding) would move them by percents.  Every
 // operand is therefore a pair of binary16 halves, hi + lo, 22 bits, and a
-// product is hi hi + hi lo + lo hi in one float32 accumulator; the error of the
-// result is below 2e-4 of its norm also for spectra that fall off by 1e4
-// (a rounding of the bfloat16 result itself is 1.7e-3).  Scales are powers of
-// two that keep the halves clear of binary16's ends: G is scaled to root mean
-// square 1 (its largest entry is then at most sqrt(m n)), A, q and A q by 2^13
-// (their eigenvalues stay below 3.5), Q_k by what a^k leaves.
+// product is lo hi + hi lo + hi hi in one float32 accumulator, the low halves
+// first because the accumulator truncates.  p is kept rather than q, whose
+// diagonal would round by a 2^-23, and the products are made exactly symmetric.
+// Measured against binary64, as parts of the result's norm: 1.7e-3, which is the
+// rounding to bfloat16, for Gaussian and gradient-like matrices; at most 2.2e-3
+// for spectra that fall off by 1e4 or have one dominant value (plain bfloat16
+// iterations: 2e-2 to 2e-1).  Scales are powers of two that keep the halves clear
+// of binary16's ends: G is scaled to root mean square 1 (its largest entry is
+// then at most sqrt(m n)), A, p and T by 2^13 (their eigenvalues stay below 3),
+// Q_k by what a^k leaves.
 // bfloat16 G is scaled by a power of two, which makes its high half exact and
 // its low half zero: one product for A_0 instead of three, two for X_0 Q.
 //
 // A matrix of at most 24,576 elements and rank at most 64 is done whole by one
 // block, in float32 from shared memory (one launch instead of five: 4 matrices
-// of 512 x 16 took 49 us in five).  Ranks up to 64 otherwise run the n x n part
-// in one block per matrix, in float32 FMAs;
-// larger ranks as launches over all matrices (three per step), on CTA pairs.
+// of 512 x 16 took 49 us in five, 21 us so).  Ranks up to 64 otherwise run the
+// n x n part in one block per matrix, in float32 FMAs; larger ranks as launches
+// over all matrices (three a step), on CTA pairs.  (One launch for all steps,
+// whose units wait for the earlier ones of their own matrix, was no faster: 243
+// against 229 us for four odd matrices, 2590 against 2530 us for the 28 of a
+// block: a step's latency is in the tiles, not in the launches.)
+//
+// Three products of halves cost 96 KB of copies for 64 k of a tile where one
+// would cost 32, so the n x n products run at the copies' rate: 57 us a launch
+// for 28 matrices (12 of rank 800, 16 of rank 544).
 
 #include <algorithm>
 #include <cmath>
@@ -50,7 +61,7 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr int kMostMats = 64, kMostGroups = 8;   // of one set of launches
 constexpr int kNormBlocks = 592;                 // blocks (and partial sums) a matrix has at most
 constexpr int kSmallN = 64;
-constexpr float kSA = 8192.0f;                   // scale of A, q and A q
+constexpr float kSA = 8192.0f;                   // scale of A, p and T
 constexpr int kMaxSteps = 10;
 
 // One matrix as the elementwise kernels see it.
