@@ -96,18 +96,20 @@ __global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restr
     const int per = (int)(((long long)V + gridDim.x - 1) / gridDim.x);
     const long long r0 = (long long)blockIdx.x * per, r1 = min((long long)V, r0 + per);   // rows of this block
     const int first = (int)min((long long)kZeroRows, max(0LL, r1 - r0));
-    const bool wide = row_bytes % 16 == 0 && ((uintptr_t)out & 15) == 0;
-    // zeros in the rows [v0, v0 + rows) without a token, by the threads t, t + n, ...; 128 threads a row
+    // zeros in the rows [v0, v0 + rows) without a token, by the threads t, t + n, ..; `lanes` threads a row
+    int lanes = 4;
+    while (lanes < 128 && (size_t)lanes * 16 < row_bytes) lanes <<= 1;
     auto zeros = [&](long long v0, int rows, int t, int n) {
-        for (int r = t >> 7; r < rows; r += n >> 7) {
+        for (int r = t / lanes; r < rows; r += n / lanes) {
             if (seen[r]) continue;
             unsigned char *const dst = out + (v0 + r) * row_bytes;
-            if (wide) {
-                for (size_t i = t & 127; i < row_bytes / 16; i += 128)
-                    reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
-            } else {
-                for (size_t i = t & 127; i < row_bytes / 2; i += 128) reinterpret_cast<uint16_t *>(dst)[i] = 0;
-            }
+            // to the first 16-byte boundary and from the last one in elements of 2 bytes
+            const size_t head = min((size_t)(-(uintptr_t)dst & 15), row_bytes), body = (row_bytes - head) / 16;
+            const size_t l = t & (lanes - 1);
+            for (size_t i = l; i < head / 2; i += lanes) reinterpret_cast<uint16_t *>(dst)[i] = 0;
+            for (size_t i = l; i < body; i += lanes) reinterpret_cast<uint4 *>(dst + head)[i] = make_uint4(0, 0, 0, 0);
+            for (size_t i = head + body * 16 + 2 * l; i < row_bytes; i += 2 * lanes)
+                *reinterpret_cast<uint16_t *>(dst + i) = 0;
         }
     };
     pdl_go();
@@ -265,14 +267,12 @@ __global__ void __launch_bounds__(256) join_kernel(const unsigned long long *__r
     const uint32_t id = (uint32_t)(pairs[lastp] >> 32);
     if ((int)id >= V || (uint32_t)(pairs[lastp + 1] >> 32) != id) return;   // nothing goes on
     if (b > 0 && (uint32_t)(pairs[b * kPairs - 1] >> 32) == id) return;     // it began before this block
-    // last block that holds a pair of this token: pairs are sorted, so search for the first larger id
-    long long lo = lastp + 1, hi = M;
-    while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        if ((uint32_t)(pairs[mid] >> 32) <= id) lo = mid + 1;
-        else hi = mid;
+    // last block that holds a pair of this token: the blocks whose first pair is one follow each other
+    long long e = b;
+    for (int more = 256; more == 256; e += more) {
+        const long long q = e + 1 + threadIdx.x;
+        more = __syncthreads_count(q * kPairs < M && (uint32_t)(pairs[q * kPairs] >> 32) == id);
     }
-    const long long e = (lo - 1) / kPairs;
     const int c = blockIdx.y * 256 + threadIdx.x;
     if (c >= D / N) return;
     Vec<float, N> a = reinterpret_cast<const Vec<float, N> *>(part + (2 * b + 1) * D)[c];

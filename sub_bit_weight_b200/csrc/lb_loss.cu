@@ -463,14 +463,20 @@ __global__ void __launch_bounds__(256) round_sum_kernel(const float4 *__restrict
 // ---- host
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// What a unit of the two products costs, in 64-deep k blocks of a pair (0.27 us): its k blocks, but at least its epilogue,
+// 2.4 us for 256 x 256 outputs, which is all there is where few rows are contracted into dW.
+constexpr long kEpilogueBlocks = 9;
+long unit_cost(long kb) { return std::max(kb, kEpilogueBlocks); }
+
 // K ranges of dH: k is the whole vocabulary, so a few rows give few, long tiles.  The time of `s` ranges in 64-deep k
-// blocks of a pair (0.41 us): the launch's longest chain, plus the write and read of the fp32 partial results at the
-// copy rate (2.7 MB in that time), which one range does not need.  Measured at M = 16, D = 8192, V = 32000 (frozen W).
+// blocks of a pair: the launch's longest chain, plus the write and read of the fp32 partial results at the copy rate
+// (1.8 MB in that time), which one range does not need.  With M = 777, D = 1160, V = 32003 (20 tiles of 501 k blocks, 7
+// ranges) the product takes 62 us and the adding 7; whole, a chain of 501 k blocks alone would be 135.
 int dh_splits(int M, int D, int V, bool with_dW, int pairs)
 {
     const long tiles = (long)((M + kMmTile - 1) / kMmTile) * ((D + kMmTile - 1) / kMmTile);
     const long nkb = ((long)V + kMmBK - 1) / kMmBK;
-    const long dw_len = (M + kMmBK - 1) / kMmBK;
+    const long dw_len = unit_cost((M + kMmBK - 1) / kMmBK);
     const double dw = with_dW ? (double)((V + kMmTile - 1) / kMmTile) * ((D + kMmTile - 1) / kMmTile) * dw_len : 0.0;
     int best = 1;
     double best_cost = 1e300;
@@ -478,7 +484,7 @@ int dh_splits(int M, int D, int V, bool with_dW, int pairs)
         const long len = (nkb + s - 1) / s, units = tiles * s;
         const double chain = (double)((units + pairs - 1) / pairs) * len;
         const double even = ((double)units * len + dw) / pairs + (with_dW ? dw_len : 0);
-        const double cost = std::max(chain, even) + (s > 1 ? 8.0 + (double)s * M * D * 8.0 / 2.7e6 : 0.0);
+        const double cost = std::max(chain, even) + (s > 1 ? 8.0 + (double)s * M * D * 8.0 / 1.8e6 : 0.0);
         if (cost < best_cost) {
             best_cost = cost;
             best = s;
@@ -660,7 +666,8 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
         const cudaError_t e = mm_pairs(&pairs);
         if (e != cudaSuccess) return status_from(e);
         const int n1 = mm_units(Q), more = G.nunits % pairs;
-        if (more) G.extra = (int)std::min<long>((P.kb_per + Q.kb_per / 2) / Q.kb_per, n1 / (pairs - more));
+        const long c0 = unit_cost(P.kb_per), c1 = unit_cost(Q.kb_per);
+        if (more) G.extra = (int)std::min<long>((c0 + c1 / 2) / c1, n1 / (pairs - more));
         G.n = 2;
         G.nunits += n1;
         if (pairs > G.nunits) G.extra = 0;   // fewer pairs are launched than the rule above counted with

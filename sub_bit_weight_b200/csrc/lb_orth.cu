@@ -504,72 +504,110 @@ __global__ void __launch_bounds__(256) gram_kernel(const __grid_constant__ Group
     }
 }
 
-// ---- n <= 64: the whole polynomial in one block of 1024 threads, float32
-// Thread (ty, tx) has the elements (ty + 32 a, tx + 32 b) on and above the diagonal, and writes each to both its places (see
-// OrthEpi).  A row's threads read one word of X together and 32 words of Y side by side; a pitch of 65 spreads the columns
-// that the mirror images go to over all banks.
-constexpr int kSmallP = 65;
+// ---- n <= 64: the whole polynomial in one block of 1024 threads, float32 from shared memory
+// Only elements on and above the diagonal are computed, each written to both its places (see OrthEpi).  Up to rank 32 a
+// thread has one of them: a product is then as long as one dot product (4 matrices of 512 x 16: 27 us with 4 x 4 elements
+// a thread, 21 us so).  Above, 256 of the threads have 4 x 4 each, since one word of shared memory per multiply-add would
+// bound the products (4 of 64 x 64: 127 us with single elements, 60 us so).
+// Rows are 68 words apart, so that 4 columns can be read at once.
+constexpr int kSmallP = 68;
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallMat = 64 * kSmallP;
 
-// c = s X Y + t D for symmetric X (its row k serves as its column k)
-__device__ __forceinline__ void small_mul(const float *X, const float *Y, const float *D, float s, float t, int n,
-                                          float (&c)[2][2])
-{
-    const int ty = threadIdx.x >> 5, tx = threadIdx.x & 31;
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = a; b < 2; ++b) {
-            const int i = ty + 32 * a, j = tx + 32 * b;
-            if (i >= n || j >= n || i > j) continue;
-            float u = 0.0f, v = 0.0f;
-            int k = 0;
+struct SmallOne {
+    float c;
+    int i, j;
+    bool mine;
+    __device__ __forceinline__ SmallOne(int n) : c(0.0f), i(threadIdx.x >> 5), j(threadIdx.x & 31), mine(i <= j && j < n) {}
+    // c = s X Y + t D for symmetric X (its row k serves as its column k)
+    __device__ __forceinline__ void mul(const float *X, const float *Y, const float *D, float s, float t, int n)
+    {
+        if (!mine) return;
+        float u = 0.0f, v = 0.0f;
+        int k = 0;
 #pragma unroll 4
-            for (; k + 1 < n; k += 2) {
-                u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
-                v = fmaf(X[(k + 1) * kSmallP + i], Y[(k + 1) * kSmallP + j], v);
-            }
-            if (k < n) u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
-            c[a][b] = fmaf(s, u + v, t * D[i * kSmallP + j]);
+        for (; k + 1 < n; k += 2) {
+            u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
+            v = fmaf(X[(k + 1) * kSmallP + i], Y[(k + 1) * kSmallP + j], v);
         }
-}
+        if (k < n) u = fmaf(X[k * kSmallP + i], Y[k * kSmallP + j], u);
+        c = fmaf(s, u + v, t * D[i * kSmallP + j]);
+    }
+    __device__ __forceinline__ void put(float *D, int, float diagonal = 0.0f) const
+    {
+        if (mine) D[i * kSmallP + j] = D[j * kSmallP + i] = c + (i == j ? diagonal : 0.0f);
+    }
+};
 
-__device__ __forceinline__ void small_put(float *D, int n, const float (&c)[2][2], float diagonal = 0.0f)
-{
-    const int ty = threadIdx.x >> 5, tx = threadIdx.x & 31;
+struct SmallTile {
+    float c[4][4];
+    int ty, tx;
+    bool mine;
+    __device__ __forceinline__ SmallTile(int n) : ty(threadIdx.x >> 4), tx(threadIdx.x & 15), mine(ty <= tx && 4 * tx < n) {}
+    __device__ __forceinline__ void mul(const float *X, const float *Y, const float *D, float s, float t, int n)
+    {
+        if (!mine) return;
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int b = a; b < 2; ++b) {
-            const int i = ty + 32 * a, j = tx + 32 * b;
-            if (i >= n || j >= n || i > j) continue;
-            D[i * kSmallP + j] = D[j * kSmallP + i] = c[a][b] + (i == j ? diagonal : 0.0f);
+            for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(X + k * kSmallP + 4 * ty);
+            const float4 y = *reinterpret_cast<const float4 *>(Y + k * kSmallP + 4 * tx);
+            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) c[i][j] = fmaf(xs[i], ys[j], c[i][j]);
         }
-}
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[i][j] = fmaf(s, c[i][j], t * D[(4 * ty + i) * kSmallP + 4 * tx + j]);
+    }
+    __device__ __forceinline__ void put(float *D, int n, float diagonal = 0.0f) const
+    {
+        if (!mine) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * ty + i <= 4 * tx + j && 4 * tx + j < n)
+                    D[(4 * ty + i) * kSmallP + 4 * tx + j] = D[(4 * tx + j) * kSmallP + 4 * ty + i] =
+                        c[i][j] + (4 * ty + i == 4 * tx + j ? diagonal : 0.0f);
+    }
+};
 
 // Q_steps from A (shared memory, kSmallMat floats each; p and T are scratch); ends synchronised
-__device__ __forceinline__ void small_chain(float *A, float *p, float *T, float *Q, int n, int steps)
+template <class E>
+__device__ __forceinline__ void small_chain_of(float *A, float *p, float *T, float *Q, int n, int steps)
 {
-    float c[2][2], d[2][2];
+    E c(n), d(n);
     for (int k = 0; k < steps; ++k) {
-        small_mul(A, A, A, kC, kB, n, c);
-        small_put(p, n, c);
-        if (k == 0) small_put(Q, n, c, kA);
+        c.mul(A, A, A, kC, kB, n);
+        c.put(p, n);
+        if (k == 0) c.put(Q, n, kA);
         __syncthreads();
-        if (k > 0) small_mul(Q, p, Q, 1.0f, kA, n, d);
+        if (k > 0) d.mul(Q, p, Q, 1.0f, kA, n);
         if (k + 1 < steps) {
-            small_mul(A, p, A, 1.0f, kA, n, c);
-            small_put(T, n, c);
+            c.mul(A, p, A, 1.0f, kA, n);
+            c.put(T, n);
         }
         __syncthreads();
-        if (k > 0) small_put(Q, n, d);
+        if (k > 0) d.put(Q, n);
         if (k + 1 < steps) {
-            small_mul(T, p, T, 1.0f, kA, n, c);
-            small_put(A, n, c);
+            c.mul(T, p, T, 1.0f, kA, n);
+            c.put(A, n);
         }
         __syncthreads();
     }
+}
+
+__device__ __forceinline__ void small_chain(float *A, float *p, float *T, float *Q, int n, int steps)
+{
+    if (n <= 32) small_chain_of<SmallOne>(A, p, T, Q, n, steps);
+    else small_chain_of<SmallTile>(A, p, T, Q, n, steps);
 }
 
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ Groups P, int steps, float q_scale)
