@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats
         float x[8];
         if (wide_loads) {
             const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(m.G) + g);
-            const float4 u = src[0];
-            const float4 v = col + 4 < m.cols ? src[1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float4 u = col < m.cols ? src[0] : zero, v = col + 4 < m.cols ? src[1] : zero;
             x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
             x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
         } else {

@@ -466,6 +466,17 @@ def test_orthogonalise_unaligned(lib):
         assert float(buf[0]) == -7.0 and bool((buf[1 + m * n:] == -7.0).all())
 
 
+@pytest.mark.parametrize("rows,cols", [(65536, 72), (72, 65536), (16384, 800), (32768, 44)])
+def test_orthogonalise_matrix_at_the_end_of_its_memory(lib, rows, cols):
+    """Matrices that fill their 2 MB pages to the last byte, so that a read past the end is a read of unmapped memory."""
+    assert rows * cols * 4 % (1 << 21) == 0 or cols == 44
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    G = torch.randn(rows, cols, generator=_gen(rows), device="cuda")
+    out, = lib.lb_orthogonalise([G])
+    assert _off(out, _orth_ref(G)) <= SMOOTH
+
+
 # ---------------------------------------------------------------------------------------------- calls in earnest
 
 def _all_calls(lib, seed):
