@@ -41,8 +41,9 @@
 //
 // A problem is a batch of equal products, its operands arrays [z][row][column].
 // With parts = 3 each operand is a pair of halves (the planes z and z + 1: high
-// and low), and lo * hi + hi * lo + hi * hi runs as one main loop three times as
-// long; with parts = 2 one operand is whole and only the other has a low half.
+// and low), and hi * hi + lo * hi + hi * lo is taken from one copy of the four
+// halves of a k block; with parts = 2 one operand is whole and only the other
+// has a low half.
 // A problem marked symmetric has only its tiles on and above the diagonal.
 //
 // Every wait is bounded: on timeout an error code is left in g_mm_err and
@@ -59,7 +60,7 @@ namespace lb {
 constexpr int kMmTile = 256;      // i and j of a unit
 constexpr int kMmHalf = 128;      // i and j one CTA of the pair stages
 constexpr int kMmBK = 64;         // k of a stage
-constexpr int kMmStages = 6;
+constexpr int kMmStages = 6;      // even: a k block of halves takes two
 constexpr int kMmThreads = 384;
 constexpr int kMmEpiWarps = 8;
 // Registers a thread: 168 at launch (what 12 warps can have), then 56 and 2 x 224 by group of four warps, the same sum.
@@ -72,7 +73,7 @@ constexpr uint32_t kMmSlice = kMmBK * 128;             // MN-major: 64 k rows of
 // Error code of a bounded wait that gave up, one per source file that has such kernels (mm_status).
 static __device__ int g_mm_err;
 
-// One problem of a launch: `batch` products of M x N over nkb 64-deep k blocks, three times as many with parts = 3.
+// One problem of a launch: `batch` products of M x N over nkb 64-deep k blocks.
 // a_mn / b_mn: the operand is MN-major.  za, zb: its z planes from one product of the batch to the next.
 struct MmProb {
     int a_mn, b_mn;
@@ -219,7 +220,7 @@ struct MmUnit {
     int b;             // product of its batch
     int tm, tn, split;
     int half;          // columns one CTA stages: half the tile's, fewer in the last column of tiles
-    int kb0, kb1;      // k blocks [kb0, kb1) of the concatenated segments
+    int kb0, kb1;      // k blocks [kb0, kb1)
 };
 
 template <int kMaxProbs>
@@ -280,9 +281,8 @@ __device__ __forceinline__ MmUnit mm_unit(const MmProb *p, int nprobs, int u)
         r.tn = local - r.tm * P.ntn;
     }
     r.half = min(P.width, (P.N - r.tn * P.width + 31) & ~31) >> 1;
-    const int total = P.nkb * P.parts;
     r.kb0 = r.split * P.kb_per;
-    r.kb1 = min(total, r.kb0 + P.kb_per);
+    r.kb1 = min(P.nkb, r.kb0 + P.kb_per);
     return r;
 }
 
@@ -362,35 +362,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 const bool mn = is_a ? P.a_mn != 0 : P.b_mn != 0;
                 const bool two = mn && (is_a || U.half > 64);   // both 64-wide slices
                 const int x0 = is_a ? U.tm * kMmTile + (int)rank * kMmHalf : U.tn * P.width + (int)rank * U.half;
-                // both CTAs' halves of both operands; a K-major box of B has width / 2 rows
-                const uint32_t bytes =
-                    2 * (kMmOperand + (P.b_mn ? (U.half > 64 ? 2 : 1) * kMmSlice : P.width * kMmBK));
-                const int nkb = P.nkb, parts = P.parts, z0 = U.b * (is_a ? P.za : P.zb);
-                // low halves first (the accumulator truncates by what is already in it): with three parts
-                // lo * hi, hi * lo, hi * hi; with two the operand that has a low half
-                const int low = parts == 3 ? (is_a ? 0 : 1) : parts == 2 && (is_a == (P.b_whole != 0)) ? 0 : -1;
-                int seg = U.kb0 / nkb, kb = U.kb0 - seg * nkb;
-                for (int left = U.kb1 - U.kb0; left > 0; --left) {
-                    if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
-                    const bool one = elect_one();
-                    if (one && is_a && rank == 0) mbar_expect_tx(&S.full[s], bytes);
-                    unsigned char *const dst = base + s * kMmOperand;
-                    const uint32_t bar = full0 + s * 8;
-                    const int k = kb * kMmBK, z = z0 + (seg == low ? 1 : 0);
-                    if (one) {
-                        tma_load_3d_pair(dst, map, mn ? x0 : k, mn ? k : x0, z, bar);
-                        if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z, bar);
+                // both CTAs' halves; a K-major box of B has width / 2 rows
+                const uint32_t bytes_b = P.b_mn ? (U.half > 64 ? 2 : 1) * kMmSlice : P.width * kMmBK;
+                const bool low_a = P.parts == 3 || (P.parts == 2 && P.b_whole), low_b = P.parts == 3 || (P.parts == 2 && !P.b_whole);
+                const uint32_t bytes[2] = {2 * (kMmOperand + bytes_b), 2 * ((low_a ? kMmOperand : 0) + (low_b ? bytes_b : 0))};
+                const int planes = P.parts > 1 ? 2 : 1, z0 = U.b * (is_a ? P.za : P.zb);
+                const bool low = is_a ? low_a : low_b;
+                for (int kb = U.kb0; ok && kb < U.kb1; ++kb)
+                    for (int plane = 0; plane < planes; ++plane) {
+                        if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
+                        const bool one = elect_one();
+                        if (one && is_a && rank == 0) mbar_expect_tx(&S.full[s], plane ? bytes[1] : bytes[0]);
+                        unsigned char *const dst = base + s * kMmOperand;
+                        const uint32_t bar = full0 + s * 8;
+                        const int k = kb * kMmBK;
+                        if (one && (plane == 0 || low)) {
+                            tma_load_3d_pair(dst, map, mn ? x0 : k, mn ? k : x0, z0 + plane, bar);
+                            if (two) tma_load_3d_pair(dst + kMmSlice, map, x0 + 64, k, z0 + plane, bar);
+                        }
+                        __syncwarp();
+                        if (++s == kMmStages) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
-                    __syncwarp();
-                    if (++kb == nkb) {
-                        kb = 0;
-                        ++seg;
-                    }
-                    if (++s == kMmStages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
             }
             if (*abort) {
                 // let the copies already issued land before the pair leaves: a wait gives up after two seconds, a copy
@@ -413,26 +408,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                     const uint64_t step_a = a_mn ? 2048 >> 4 : 32 >> 4, step_b = b_mn ? 2048 >> 4 : 32 >> 4;
                     const uint64_t da0 = a_mn ? smem_desc_mn_sw128(S.A[0], kMmSlice) : smem_desc_sw128(S.A[0]);
                     const uint64_t db0 = b_mn ? smem_desc_mn_sw128(S.B[0], kMmSlice) : smem_desc_sw128(S.B[0]);
-                    const int chunk = P.chunk;
+                    const int chunk = P.chunk, parts = P.parts;
+                    const bool low_a = parts == 3 || (parts == 2 && P.b_whole), low_b = parts == 3 || (parts == 2 && !P.b_whole);
                     for (int left = U.kb1 - U.kb0; ok && left > 0; left -= chunk, ++acc) {
                         const int ab = acc & 1;
                         if (!(ok = mbar_wait_warp(&S.acce[ab], ((acc >> 1) & 1) ^ 1, abort, err, 2))) break;
                         tc_fence_after();
                         const uint32_t dacc = tmem + (uint32_t)(ab * kMmTile);
                         uint32_t add = 0;
+                        // A k block is one stage of the ring, or two, the high halves and the low ones.
+                        auto products = [&](uint32_t sa, uint32_t sb) {
+                            const uint64_t da = da0 + sa * (kMmOperand >> 4), db = db0 + sb * (kMmOperand >> 4);
+                            tc_mma_f16_pair(dacc, da, db, idesc, add);
+#pragma unroll
+                            for (int kk = 1; kk < kMmBK / 16; ++kk)
+                                tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, 1u);
+                            add = 1;
+                        };
                         for (int i = min(left, chunk); i > 0; --i) {
                             if (!(ok = mbar_wait_warp(&S.full[s], ph, abort, err, 3))) break;
                             tc_fence_after();
-                            const uint64_t da = da0 + s * (kMmOperand >> 4), db = db0 + s * (kMmOperand >> 4);
-                            if (elect_one()) {
-                                tc_mma_f16_pair(dacc, da, db, idesc, add);
-#pragma unroll
-                                for (int kk = 1; kk < kMmBK / 16; ++kk)
-                                    tc_mma_f16_pair(dacc, da + kk * step_a, db + kk * step_b, idesc, 1u);
-                                tc_commit_pair(&S.empty[s]);
+                            if (parts == 1) {
+                                if (elect_one()) {
+                                    products(s, s);
+                                    tc_commit_pair(&S.empty[s]);
+                                }
+                                add = 1;
+                            } else {
+                                const uint32_t lo = s + 1;   // kMmStages is even
+                                if (elect_one()) products(s, s);
+                                add = 1;
+                                __syncwarp();
+                                if (!(ok = mbar_wait_warp(&S.full[lo], ph, abort, err, 3))) break;
+                                tc_fence_after();
+                                if (elect_one()) {
+                                    if (low_a) products(lo, s);
+                                    if (low_b) products(s, lo);
+                                    tc_commit_pair(&S.empty[s]);
+                                    tc_commit_pair(&S.empty[lo]);
+                                }
+                                ++s;
                             }
                             __syncwarp();
-                            add = 1;
                             if (++s == kMmStages) {
                                 s = 0;
                                 ph ^= 1;
@@ -520,9 +537,8 @@ inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int
     P.chunk = kMmChunkAll;
     P.m_fast = m_fast ? 1 : 0;
     P.unit0 = unit0;
-    const int total = P.nkb * parts;
-    P.kb_per = (total + splits - 1) / splits;
-    P.splits = (total + P.kb_per - 1) / P.kb_per;
+    P.kb_per = (P.nkb + splits - 1) / splits;
+    P.splits = (P.nkb + P.kb_per - 1) / P.kb_per;
 }
 // Host: CTA pairs that run at once on the current device.
 inline cudaError_t mm_pairs(int *pairs)

@@ -847,13 +847,20 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             out.push_back(std::move(C));
             continue;
         }
-        // Ranges of the Gram products.  In k blocks of a pair (0.27 us): the longest list of units as they are dealt, and
-        // the writing and reading of the ranges' partial sums at the copy rate.  Units of at least 24 k blocks.
+        // Ranges of the Gram products, in products of 64 deep by a pair (0.27 us): the longest list of units as they are
+        // dealt, and the writing and reading of the ranges' partial sums at the copy rate.  Units of at least 24 of them.
         const int parts = bf16 ? 1 : 3, pairs = 74;
+        auto blocks = [&](const Group &g) { return (long)(g.m + kMmBK - 1) / kMmBK; };
+        auto tiles = [&](const Group &g) {
+            const int nt = (g.n + kMmTile - 1) / kMmTile;
+            return (long)mm_tiles(nt, nt, true, kMmTile) * g.batch;
+        };
+        auto cut = [&](const Group &g, long unit) {   // as mm_plan cuts
+            const long k = blocks(g), r = std::min(64L, (k * parts + unit - 1) / unit), per = (k + r - 1) / r;
+            return (k + per - 1) / per;
+        };
         double total = 0.0;
-        for (const Group &g : C.groups)
-            total += (double)mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + kMmTile - 1) / kMmTile, true, kMmTile) * g.batch *
-                     parts * ((g.m + kMmBK - 1) / kMmBK);
+        for (const Group &g : C.groups) total += (double)tiles(g) * blocks(g) * parts;
         long unit = 24;
         double best = 1e300;
         for (int c = 1; c <= 12; ++c) {
@@ -862,9 +869,8 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             double bytes = 0.0;
             long at_unit = 0;
             for (const Group &g : C.groups) {
-                const long k = (long)parts * ((g.m + kMmBK - 1) / kMmBK), r = std::min(64L, (k + u - 1) / u), per = (k + r - 1) / r;
-                const long tiles = mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + kMmTile - 1) / kMmTile, true, kMmTile);
-                for (long x = 0; x < tiles * g.batch * r; ++x) load[at_unit++ % pairs] += (double)per + 4.0;
+                const long r = cut(g, u);
+                for (long x = 0; x < tiles(g) * r; ++x) load[at_unit++ % pairs] += (double)blocks(g) * parts / r + 4.0;
                 bytes += (double)r * g.batch * g.n * g.pn * 4.0 * 2.0;
             }
             const double cost = *std::max_element(load.begin(), load.end()) + bytes / 1.8e6;
@@ -883,10 +889,7 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
         C.sums = take(C.order.size() * kNormBlocks * sizeof(double));
         C.scal = take(C.order.size() * sizeof(float2));
         for (Group &g : C.groups) {
-            const long k = (long)parts * ((g.m + kMmBK - 1) / kMmBK);
-            g.ranges = (int)std::min<long>(64, (k + unit - 1) / unit);
-            const long per = (k + g.ranges - 1) / g.ranges;
-            g.ranges = (int)((k + per - 1) / per);
+            g.ranges = (int)cut(g, unit);
             const size_t nn = (size_t)g.batch * 2 * g.n * g.pn * 2;
             g.X = take((size_t)g.batch * (bf16 ? 1 : 2) * g.rows * g.pitch * 2);
             g.A = take(nn);
