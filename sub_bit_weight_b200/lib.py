@@ -609,7 +609,7 @@ def lb_embedding_forward(ids: torch.Tensor, table: torch.Tensor, scale: float = 
     V, D = table.shape
     dtype = table.dtype if dtype is None else dtype
     with _On(stream, (ids, table), ("ids", "table")) as on:
-        out = torch.empty((*ids.shape, D), dtype=dtype, device=on.device)
+        out = table.new_empty((*ids.shape, D), dtype=dtype)
         _check(_lib.lb_embedding_forward(_dev(ids, torch.int64, "ids"), ids.numel(),
                                          _dev(table, table.dtype, "table"), _element(table.dtype, "table"), V, D,
                                          float(scale), out.data_ptr(), _element(dtype, "dtype"), on.stream),
@@ -714,7 +714,8 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
     with _On(stream, G, names) as on:
         src = ptrs(*[t.data_ptr() if t.dtype is dtype and t.is_contiguous() else _dev(t, dtype, names[i])
                      for i, t in enumerate(G)])
-        out = [torch.empty(shape, dtype=torch.bfloat16, device=on.device) for shape in shapes]
+        bf16 = torch.bfloat16
+        out = [t.new_empty(shape, dtype=bf16) for t, shape in zip(G, shapes)]
         ws = _workspace(workspace, int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code)), on)
         _check(_lib.lb_orthogonalise(src, code, rows, cols, n, int(steps), float(eps), ptrs(*[t.data_ptr() for t in out]),
                                      _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream), "lb_orthogonalise")
