@@ -190,11 +190,12 @@ lb_status gemm_at_b_batch(const GemmDesc *descs, int n, int *err, cudaStream_t s
 // Launch whose set-up may overlap the end of the kernel before it on the stream.  `fn` has to call pdl_wait() before it
 // touches memory that kernel may still be using.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
+cudaError_t launch_after_smem(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -202,6 +203,11 @@ cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t s, A... args)
+{
+    return launch_after_smem(fn, grid, threads, 0, s, args...);
 }
 // Raise the dynamic shared-memory limit of kernel `fn` on the current device to at least `bytes` (never lowers
 // it; per device and kernel, thread-safe).

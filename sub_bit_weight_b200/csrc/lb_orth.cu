@@ -20,13 +20,16 @@
 // blows up (by up to a^steps = 485), and in A_0 they are squared, so an error
 // of 2^-12 in A (one binary16 rounding) would move them by percents.  Every
 // operand is therefore a pair of binary16 halves, hi + lo, 22 bits, and a
-// product is lo hi + hi lo + hi hi in one float32 accumulator, the low halves
-// first because the accumulator truncates.  p is kept rather than q, whose
+// product is hi hi + lo hi + hi lo in one float32 accumulator for each k block,
+// whose halves are copied once for the three.  p is kept rather than q, whose
 // diagonal would round by a 2^-23, and the products are made exactly symmetric.
 // Measured against binary64, as parts of the result's norm: 1.7e-3, which is the
 // rounding to bfloat16, for Gaussian and gradient-like matrices; at most 2.2e-3
 // for spectra that fall off by 1e4 or have one dominant value (plain bfloat16
-// iterations: 2e-2 to 2e-1).  Scales are powers of two that keep the halves clear
+// iterations: 2e-2 to 2e-1).  That is after five steps; singular values below
+// some 1e-3 of the norm, lifted to 1 by up to ten steps, come out with relative
+// errors of about 2^-22 over their square (1e-2 of the norm for a square Gaussian
+// matrix of rank 65 that has one).  Scales are powers of two that keep the halves clear
 // of binary16's ends: G is scaled to root mean square 1 (its largest entry is
 // then at most sqrt(m n)), A, p and T by 2^13 (their eigenvalues stay below 3),
 // Q_k by what a^k leaves.
@@ -36,15 +39,17 @@
 // A matrix of at most 24,576 elements and rank at most 64 is done whole by one
 // block, in float32 from shared memory (one launch instead of five: 4 matrices
 // of 512 x 16 took 49 us in five, 21 us so).  Ranks up to 64 otherwise run the
-// n x n part in one block per matrix, in float32 FMAs; larger ranks as launches
-// over all matrices (three a step), on CTA pairs.  (One launch for all steps,
+// n x n part in one block per matrix, in float32 FMAs (up to rank 48 faster than
+// the tensor core, 57 against 78 us a call at 4096 x 33, and 79 against 74 at
+// rank 64); ranks up to 128 in one block on its tensor core; larger ranks as
+// launches over all matrices (three a step), on CTA pairs.  (One launch for all steps,
 // whose units wait for the earlier ones of their own matrix, was no faster: 243
 // against 229 us for four odd matrices, 2590 against 2530 us for the 28 of a
 // block: a step's latency is in the tiles, not in the launches.)
 //
-// Three products of halves cost 96 KB of copies for 64 k of a tile where one
-// would cost 32, so the n x n products run at the copies' rate: 57 us a launch
-// for 28 matrices (12 of rank 800, 16 of rank 544).
+// Copied once, the four halves of 64 k of a tile are 64 KB for three products'
+// 1536 cycles of the tensor cores (copied for each product they would be 96):
+// about 60 us a launch for 28 matrices (12 of rank 800, 16 of rank 544).
 
 #include <algorithm>
 #include <cmath>
@@ -444,9 +449,10 @@ struct Groups {
     GroupArg g[kMostGroups];
     int n;
     const float2 *scal;
+    float q_scale[kMaxSteps + 1];   // after each step, for mid_kernel
 };
 
-// n > 64: 64 x 64 blocks on and above the diagonal, written to both places
+// n > 128: 64 x 64 blocks on and above the diagonal, written to both places
 __global__ void __launch_bounds__(256) gram_kernel(const __grid_constant__ Groups P)
 {
     __shared__ float tile[64][65];
@@ -643,6 +649,261 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
             D[(size_t)i * g.pn + j] = hi;
             D[plane + (size_t)i * g.pn + j] = lo;
         }
+    }
+}
+
+// ---- 64 < n <= 128: the whole polynomial in one block, on its tensor core
+// A (and T over it), p and Q stay in shared memory as binary16 halves in the tensor core's layout, 64 KB each, padded with
+// zeros to 128.  A product is 24 MMAs of 128 x 128 x 16 (1500 cycles, the tensor core's rate), its epilogue 2750: it adds
+// the linear term from the operand it replaces and writes each element of one triangle to both places.  Q's epilogue runs
+// beside the product T p, and T's beside Q p.  Three launches a step took 113 to 161 us a call for one to four matrices of
+// rank 65 to 100, this 71 to 93 (ranks above 128 would not fit).  The epilogue is not inlined: ten copies
+// of it ran out of the instruction caches, at 4200 cycles each.
+constexpr int kMidN = 128, kMidThreads = 512;
+constexpr uint32_t kMidPlane = 2 * 128 * 128;      // one plane: two blocks of 64 k, 128 rows of 128 bytes each
+constexpr uint32_t kMidSlot = 2 * kMidPlane;       // high and low
+constexpr size_t kMidSmemBytes = 3 * kMidSlot + 1024 + 64;
+
+__device__ __forceinline__ uint32_t mid_at(int row, int col)   // byte of an element in its plane
+{
+    return (uint32_t)(col >> 6) * 16384u + (uint32_t)row * 128u + (uint32_t)((((col & 63) >> 3) ^ (row & 7)) << 4) +
+           (uint32_t)(col & 7) * 2u;
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint16_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;\n" ::"r"(addr), "h"(v) : "memory");
+}
+
+// acc = X Y for symmetric X and Y: the three products of their halves
+__device__ __forceinline__ void mid_mma(uint32_t acc, const unsigned char *X, const unsigned char *Y)
+{
+    constexpr uint32_t idesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    uint32_t add = 0;
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {   // low halves first: the accumulator truncates
+        const uint64_t dx = smem_desc_sw128(X + (part == 0 ? kMidPlane : 0)), dy = smem_desc_sw128(Y + (part == 1 ? kMidPlane : 0));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint64_t off = (uint64_t)((k >> 2) * (16384 >> 4) + (k & 3) * (32 >> 4));
+            tc_mma_f16(acc, dx + off, dy + off, idesc, add);
+            add = 1;
+        }
+    }
+}
+
+// D = alpha * accumulator + beta * C + diagonal * I, of a 32 x 32 block, a row a lane, to both its places.  D may be C: an
+// element and its mirror are read and written by this warp only, and it reads each before it writes it.
+template <bool kDiag>
+__device__ __noinline__ void mid_block(uint32_t acc, uint32_t C, uint32_t D, int row, int col0, float alpha, float beta,
+                                          float diagonal)
+{
+    uint32_t v[32];
+    tmem_ld32(acc, v);
+    const uint32_t low_row = (uint32_t)(row >> 6) * 16384u + (uint32_t)(row & 7) * 2u, chunk = (uint32_t)(row & 63) >> 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c0 = col0 + 8 * i;
+        const uint32_t at = mid_at(row, c0);
+        const uint4 h = lds128(C + at), l = lds128(C + kMidPlane + at);
+        const uint32_t ch[4] = {h.x, h.y, h.z, h.w}, cl[4] = {l.x, l.y, l.z, l.w};
+        uint32_t oh[4], ol[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 fh = __half22float2(*reinterpret_cast<const __half2 *>(&ch[j]));
+            const float2 fl = __half22float2(*reinterpret_cast<const __half2 *>(&cl[j]));
+            float2 x = make_float2(fmaf(__uint_as_float(v[8 * i + 2 * j]), alpha, beta * (fh.x + fl.x)),
+                                   fmaf(__uint_as_float(v[8 * i + 2 * j + 1]), alpha, beta * (fh.y + fl.y)));
+            if (kDiag) {
+                x.x += c0 + 2 * j == row ? diagonal : 0.0f;
+                x.y += c0 + 2 * j + 1 == row ? diagonal : 0.0f;
+            }
+            const __half2 hi = __float22half2_rn(x);
+            const float2 back = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn(x.x - back.x, x.y - back.y);
+            oh[j] = *reinterpret_cast<const uint32_t *>(&hi);
+            ol[j] = *reinterpret_cast<const uint32_t *>(&lo);
+        }
+        if (kDiag) {
+            __syncwarp();   // a lane's mirrors are in the others' rows
+        } else {
+            sts128(D + at, make_uint4(oh[0], oh[1], oh[2], oh[3]));
+            sts128(D + kMidPlane + at, make_uint4(ol[0], ol[1], ol[2], ol[3]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint16_t hi = (uint16_t)(j & 1 ? oh[j / 2] >> 16 : oh[j / 2]), lo = (uint16_t)(j & 1 ? ol[j / 2] >> 16 : ol[j / 2]);
+            const uint32_t mirror = D + low_row + (uint32_t)(c0 + j) * 128u + ((chunk ^ (uint32_t)j) << 4);
+            if (!kDiag || c0 + j >= row) {
+                sts16(mirror, hi);
+                sts16(mirror + kMidPlane, lo);
+            }
+            if (kDiag && c0 + j > row) {
+                sts16(D + at + 2 * j, hi);
+                sts16(D + kMidPlane + at + 2 * j, lo);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMidThreads, 1) mid_kernel(const __grid_constant__ Groups P, int steps)
+{
+    extern __shared__ __align__(1024) unsigned char mid_raw[];
+    __shared__ uint64_t bars[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const uint32_t raw = smem_u32(mid_raw);
+    unsigned char *const A = mid_raw + (((raw + 1023u) & ~1023u) - raw), *const Pm = A + kMidSlot, *const Q = Pm + kMidSlot;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    volatile int *abort = &abort_flag;
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;\n" ::"r"(smem_u32(&tmem_base)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    pdl_go();
+    pdl_wait();
+    int w = 0;
+    for (int i = 1; i < P.n; ++i)
+        if ((int)blockIdx.x >= P.g[i].b0) w = i;
+    const GroupArg &g = P.g[w];
+    const int b = blockIdx.x - g.b0, n = g.n;
+    const float f = P.scal[g.first + b].y;
+    const size_t plane = (size_t)n * g.pn;
+    const uint32_t sA = smem_u32(A), sP = smem_u32(Pm), sQ = smem_u32(Q);
+    // A_0 from the partial sums, on and above the diagonal; zeros around it.  Rows of four elements, four rows and four
+    // ranges of a thread in flight together.
+    constexpr int kRows = 4, kAtOnce = 4;
+    const int jq = lane * 4;
+    const size_t range = (size_t)g.batch * plane;
+    for (int i0 = warp; i0 < kMidN; i0 += kRows * (kMidThreads / 32)) {
+        float4 a[kRows];
+        bool in[kRows];
+        const float *src[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int i = i0 + u * (kMidThreads / 32);
+            a[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            in[u] = i < n && jq < g.pn && jq + 3 >= i;
+            src[u] = g.part + (size_t)b * plane + (size_t)i * g.pn + jq;
+        }
+        for (int r = 0; r < g.ranges; r += kAtOnce) {
+            float4 v[kAtOnce][kRows];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    v[q][u] = in[u] && r + q < g.ranges ? *reinterpret_cast<const float4 *>(src[u] + (r + q) * range)
+                                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) a[u].x += v[q][u].x, a[u].y += v[q][u].y, a[u].z += v[q][u].z, a[u].w += v[q][u].w;
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int i = i0 + u * (kMidThreads / 32);
+            const float x[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int jc = jq + c;
+                if (jc < i) continue;
+                __half hi, lo;
+                halves(jc < n ? x[c] * f : 0.0f, hi, lo);
+                sts16(sA + mid_at(i, jc), __half_as_ushort(hi));
+                sts16(sA + kMidPlane + mid_at(i, jc), __half_as_ushort(lo));
+                sts16(sA + mid_at(jc, i), __half_as_ushort(hi));
+                sts16(sA + kMidPlane + mid_at(jc, i), __half_as_ushort(lo));
+            }
+        }
+    }
+    fence_proxy_async();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    // The 4 blocks on the diagonal and one of each mirrored pair: 3, 3, 2 and 2 for the four row quarters, each of which
+    // only the warps of one scheduler can read
+    const int quarter = warp & 3, col0 = ((quarter + (warp >> 2)) & 3) * 32, row0 = quarter * 32, row = row0 + lane;
+    const bool mine = warp < 8 || (warp < 12 && quarter < 2);
+    const uint32_t acc = tmem + ((uint32_t)row0 << 16) + (uint32_t)col0;
+    auto block = [&](uint32_t from, uint32_t C, uint32_t D, float alpha, float beta, float diagonal) {
+        if (!mine) return;
+        if (warp < 4) mid_block<true>(from, C, D, row, col0, alpha, beta, diagonal);
+        else mid_block<false>(from, C, D, row, col0, alpha, beta, 0.0f);
+    };
+    // the accumulators of bars[w] are there for every thread, or the wait gave up (bounded) and all leave
+    uint32_t phase[2] = {0, 0};
+    auto finished = [&](int w) -> bool {
+        const bool ok = mbar_wait(&bars[w], phase[w], abort, &g_mm_err, 6);
+        phase[w] ^= 1;
+        tc_fence_after();
+        return __syncthreads_and(ok) != 0;
+    };
+    // what was written is there for the next products
+    auto written = [&]() {
+        fence_proxy_async();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    };
+    // Products are issued by a warp that has no epilogue: issuing waits for the tensor core
+    auto product = [&](int w, const unsigned char *X, const unsigned char *Y) {
+        if (warp == kMidThreads / 32 - 1 && elect_one()) {
+            mid_mma(tmem + 128 * w, X, Y);
+            tc_commit(&bars[w]);
+        }
+        __syncwarp();
+    };
+    float scale = kSA;   // of Q
+    bool ok = true;
+    for (int k = 0; k < steps; ++k) {
+        // p = b A + c A^2; the first also gives Q_1 = a I + p
+        product(0, A, A);
+        if (!(ok = finished(0))) break;
+        block(acc, sA, sP, kC / kSA, kB, 0.0f);
+        if (k == 0) block(acc, sA, sQ, kC / kSA, kB, kA * kSA);
+        written();
+        // T = a A + A p over A while Q p runs, then Q <- a Q + Q p while T p runs
+        const bool more = k + 1 < steps;
+        if (more) product(0, A, Pm);
+        if (k) product(1, Q, Pm);
+        if (more) {
+            if (!(ok = finished(0))) break;
+            block(acc, sA, sA, 1.0f / kSA, kA, 0.0f);
+            written();
+            product(0, A, Pm);
+        }
+        if (k) {
+            if (!(ok = finished(1))) break;
+            const float next = P.q_scale[k + 1], fq = next / scale;
+            block(acc + 128, sQ, sQ, fq / kSA, kA * fq, 0.0f);
+            scale = next;
+        }
+        if (more) {   // A <- a T + T p
+            if (!(ok = finished(0))) break;
+            block(acc, sA, sA, 1.0f / kSA, kA, 0.0f);
+        }
+        written();
+    }
+    if (ok) {
+        __half *const D = g.A + (size_t)b * 2 * plane;
+        for (int e = tid; e < 2 * n * 16; e += kMidThreads) {   // 16-byte chunks of both planes' rows
+            const int p = e / (n * 16), r = (e / 16) % n, c = (e & 15) * 8;
+            if (c < n)
+                *reinterpret_cast<uint4 *>(D + p * plane + (size_t)r * g.pn + c) = lds128(sQ + p * kMidPlane + mid_at(r, c));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;\n" ::"r"(tmem));
     }
 }
 
@@ -954,7 +1215,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     auto square_tiles = [&](int w) {
         long t = 0;
         for (const Group &g : C.groups)
-            if (g.n > kSmallN)
+            if (g.n > kMidN)
                 t += (long)g.batch * mm_tiles((g.n + kMmTile - 1) / kMmTile, (g.n + w - 1) / w, true, w);
         return t;
     };
@@ -993,14 +1254,16 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     if ((e = launch()) != cudaSuccess) return status_from(e);
 
     // the small ranks' polynomials, the others' A_0
-    Groups big, small;
+    Groups big, mid, small;
     memset(&big, 0, sizeof(big));
+    memset(&mid, 0, sizeof(mid));
     memset(&small, 0, sizeof(small));
-    big.scal = small.scal = M.scal;
-    int bigs = 0, smalls = 0, blocks = 0;
+    big.scal = mid.scal = small.scal = M.scal;
+    for (int k = 0; k <= steps; ++k) mid.q_scale[k] = q_scale_after(k);
+    int bigs = 0, mids = 0, smalls = 0, blocks = 0;
     for (const Group &g : C.groups) {
-        const bool sm = g.n <= kSmallN;
-        Groups &to = sm ? small : big;
+        Groups &to = g.n <= kSmallN ? small : g.n <= kMidN ? mid : big;
+        int &count = g.n <= kSmallN ? smalls : g.n <= kMidN ? mids : bigs;
         GroupArg &a = to.g[to.n++];
         a.part = (const float *)(ws + g.part);
         a.A = (__half *)(ws + g.A);
@@ -1009,23 +1272,30 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         a.ranges = g.ranges;
         a.batch = g.batch;
         a.first = g.first;
-        a.b0 = sm ? smalls : bigs;
-        (sm ? smalls : bigs) += g.batch;
+        a.b0 = count;
+        count += g.batch;
         const int nb = (g.n + 63) / 64;
-        if (!sm) blocks = std::max(blocks, nb * (nb + 1) / 2);
+        if (g.n > kMidN) blocks = std::max(blocks, nb * (nb + 1) / 2);
     }
     if (bigs) {
         if ((e = launch_after(gram_kernel, dim3(blocks, bigs), 256, s, big)) != cudaSuccess) return status_from(e);
         ++*launches;
     }
+    if (mids) {
+        if ((e = ensure_dyn_smem((const void *)mid_kernel, kMidSmemBytes)) != cudaSuccess) return status_from(e);
+        if ((e = launch_after_smem(mid_kernel, dim3(mids), kMidThreads, kMidSmemBytes, s, mid, steps)) != cudaSuccess)
+            return status_from(e);
+        ++*launches;
+    }
     if (smalls) {
         const size_t smem = 4 * kSmallMat * sizeof(float);
         if ((e = ensure_dyn_smem((const void *)small_kernel, smem)) != cudaSuccess) return status_from(e);
-        small_kernel<<<smalls, kSmallThreads, smem, s>>>(small, steps, q_scale_after(steps));
+        if ((e = launch_after_smem(small_kernel, dim3(smalls), kSmallThreads, smem, s, small, steps, q_scale_after(steps))) != cudaSuccess)
+            return status_from(e);
         ++*launches;
     }
 
-    // n > 64: three launches a step
+    // n > 128: three launches a step
     // d = alpha * x y + beta * c
     auto square = [&](const Group &g, size_t x, size_t y, size_t d, float alpha, float beta, size_t c) -> OrthProb & {
         MmProb &P = B.p[B.n];
@@ -1049,7 +1319,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     for (int k = 0; bigs && k < steps; ++k) {
         begin();   // p = b A + c A^2; the first also gives Q_1 = a I + p
         for (const Group &g : C.groups) {
-            if (g.n <= kSmallN) continue;
+            if (g.n <= kMidN) continue;
             OrthProb &O = square(g, g.A, g.A, g.q, kC / kSA, kB, g.A);
             if (k == 0) {
                 O.D2 = (__half *)(ws + g.Q0);
@@ -1061,7 +1331,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         if (k + 1 == steps && k == 0) break;
         begin();   // T = a A + A p, and Q <- a Q + Q p
         for (const Group &g : C.groups) {
-            if (g.n <= kSmallN) continue;
+            if (g.n <= kMidN) continue;
             if (k + 1 < steps) square(g, g.A, g.q, g.T, 1.0f / kSA, kA, g.A);
             if (k) {
                 const size_t from = k & 1 ? g.Q0 : g.Q1, to = k & 1 ? g.Q1 : g.Q0;
@@ -1074,7 +1344,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         if (k + 1 == steps) break;
         begin();   // A <- a T + T p
         for (const Group &g : C.groups)
-            if (g.n > kSmallN) square(g, g.T, g.q, g.A, 1.0f / kSA, kA, g.T);
+            if (g.n > kMidN) square(g, g.T, g.q, g.A, 1.0f / kSA, kA, g.T);
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
     }
@@ -1084,7 +1354,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     for (const Group &g : C.groups) {
         MmProb &P = B.p[B.n];
         OrthProb &O = E.p[B.n];
-        const bool sm = g.n <= kSmallN;
+        const bool sm = g.n <= kMidN;   // Q is where A_0 would be
         const size_t Q = sm ? g.A : (steps - 1) & 1 ? g.Q1 : g.Q0;
         mm_plan(P, g.rows, g.cols, g.n, false, B.nunits, 1, bf16 ? 2 : 3, g.batch, false, wo);
         CUtensorMap mQ, mX;
@@ -1098,7 +1368,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         P.zb = g.wide ? xz : 2;
         O.kind = kOut;
         O.first = g.first;
-        O.alpha = 1.0f / (!sm && steps == 1 ? kSA : q_scale_after(steps));
+        O.alpha = 1.0f / (g.n > kSmallN && steps == 1 ? kSA : q_scale_after(steps));
         O.ldo = g.cols;
         B.nunits += mm_units(P);
         ++B.n;

@@ -402,6 +402,52 @@ def test_orthogonalise_hard_spectra(lib, m, n, kind):
     assert _off(out, _orth_ref(G)) <= 2 * 2.0 ** -8
 
 
+def _orth_bound(X, steps):
+    """Rounding to bfloat16, and what the errors of the n x n part do to this matrix, to first order.
+
+    Its symmetric operands are held to 2^-22 of their norm, and a product's truncated additions lose up to 1.5 * 2^-24 each,
+    12 on the high halves of 128 k: together below 2^-20 of the norm.  An error E of A_k counts as E / a^(2k) of A_0, whose
+    small eigenvalues grow by a^2 a step: the norms are max(lambda) at the start, at most 1.45 after, and T's roundings
+    count 1 / a more: e = 2^-20 (max(lambda) + 1.45 (1 + 1 / a) / (a^2 - 1) + 0.1).  In the singular vectors' basis the
+    result X_0 Q(A_0 + E) then moves by sigma_i E_ij (Q_i - Q_j) / (lambda_i - lambda_j), and no entry by more than twice
+    the largest singular value of a result, 1.2."""
+    a, b, c = 3.4445, -4.7750, 2.0315
+    s0 = torch.linalg.svdvals(X.double())
+    s0 = s0 / (s0.square().sum().sqrt() + 1e-7)
+    lam0 = s0.square()
+    lam, q, dlam, dq = lam0, torch.ones_like(s0), torch.ones_like(s0), torch.zeros_like(s0)
+    for _ in range(steps):   # q = Q(lambda_0) and lambda = lambda_k with their derivatives by lambda_0
+        f, df = a + b * lam + c * lam ** 2, (b + 2 * c * lam) * dlam
+        q, dq = q * f, dq * f + q * df
+        lam, dlam = lam * f ** 2, dlam * f ** 2 + 2 * lam * f * df
+    gap = lam0[:, None] - lam0[None, :]
+    near = gap.abs() <= 1e-6 * lam0[0]
+    D = torch.where(near, dq[:, None], (q[:, None] - q[None, :]) / torch.where(near, 1.0, gap))
+    e = 2.0 ** -20 * (lam0[0] + 1.45 * (1 + 1 / a) / (a * a - 1) + 0.1)
+    moved = (s0[:, None] * D * e).abs().clamp(max=2.4)
+    return 2.0 ** -8 + float(moved.norm() / (s0 * q).norm())
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 5, 10])
+def test_orthogonalise_ranks_of_one_block(lib, steps):
+    """Ranks 65 to 128, whose polynomial one block does: every edge inside its 32 x 32 blocks, few and many ranges of the
+    long axis, and a batch.  Alone or together a matrix gives the same."""
+    g = _gen(steps)
+    shapes = [(n, n) for n in (65, 95, 97, 128)] + [(260, 127), (90, 1111), (20000, 66)] + [(700, 100)] * 5 + [(500, 129)]
+    G = [torch.randn(s, generator=g, device="cuda") for s in shapes]
+    out = lib.lb_orthogonalise(G, steps=steps)
+    for i, (X, O) in enumerate(zip(G, out)):
+        assert _off(O, _orth_ref(X, steps)) <= _orth_bound(X, steps), (i, tuple(X.shape))
+    for i in (8, 3):
+        assert torch.equal(out[i], lib.lb_orthogonalise([G[i]], steps=steps)[0])
+    assert lib.lb_train_status() == lib.LB_OK
+
+
+@pytest.mark.parametrize("kind", ["1/j", "1/j2", "1e-4", "spike", "rank"])
+def test_orthogonalise_hard_spectra_of_one_block(lib, kind):
+    test_orthogonalise_hard_spectra(lib, 1024, 120, kind)
+
+
 def test_orthogonalise_singular_values(lib):
     """What the update is for: five steps bring the singular values of a gradient-like matrix near 1."""
     g = _gen(8)
