@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restr
                                                           unsigned char *__restrict__ out)
 {
     extern __shared__ __align__(16) unsigned char e_raw[];
-    int *const k = reinterpret_cast<int *>(e_raw);
+    uint32_t *const k = reinterpret_cast<uint32_t *>(e_raw);
     unsigned char *const seen = e_raw + ((chunk + 3) & ~3) * 4;
     const int tid = threadIdx.x;
     const int per = (int)(((long long)V + gridDim.x - 1) / gridDim.x);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restr
         for (int i = tid; i < n4; i += 1024) {
             long long id = i < n ? ids[base + i] : (long long)V;
             if (id < 0 || id >= V) id = V;
-            k[i] = (int)id;
+            k[i] = (uint32_t)id;
             if (id >= r0 && id - r0 < first) seen[id - r0] = 1;
         }
         __syncthreads();
@@ -132,12 +132,13 @@ __global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restr
         const int groups = kOrderThreads / split, part = tid % split;
         const uint32_t mates = (split == 32 ? ~0u : (1u << split) - 1) << ((tid & 31) - part);   // of one pair
         for (int i = blockIdx.x * groups + tid / split; i < n; i += gridDim.x * groups) {
-            const int id = k[i], at = i >> 2;
+            const uint32_t id = k[i];   // unsigned: V, and id + 1, may be 2^31 - 1 and one more
+            const int at = i >> 2;
             int count = 0;
 #pragma unroll 4
             for (int j = part; j < n4 / 4; j += split) {
-                const int4 q = reinterpret_cast<const int4 *>(k)[j];
-                const int t = id + (j < at ? 1 : 0);   // an equal id at an earlier position is smaller
+                const uint4 q = reinterpret_cast<const uint4 *>(k)[j];
+                const uint32_t t = id + (j < at ? 1 : 0);   // an equal id at an earlier position is smaller
                 if (j != at) {
                     count += (q.x < t) + (q.y < t) + (q.z < t) + (q.w < t);
                 } else {
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(1024) order_zero_kernel(const int64_t *__restr
             }
             for (int o = split >> 1; o; o >>= 1) count += __shfl_xor_sync(mates, count, o);
             if (part == 0)
-                pairs[base + count] = ((unsigned long long)(uint32_t)id << 32) | (uint32_t)(base + i);
+                pairs[base + count] = ((unsigned long long)id << 32) | (uint32_t)(base + i);
         }
     }
     if (nchunks == 0) {
