@@ -580,9 +580,18 @@ class _On:
             self._guard.__exit__(*exc)
 
 
+def _sizes(names: str, *sizes):
+    """The library's sizes are C ints, into which ctypes would cut a larger number without a word."""
+    for name, n in zip(names.split(), sizes):
+        if not 0 <= n < 1 << 31:
+            raise ValueError(f"{name} must be 0 .. 2^31 - 1, got {n}")
+
+
 def _workspace(workspace, need: int, on: _On) -> torch.Tensor:
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=on.device)
+    if workspace.device != on.device:
+        raise ValueError(f"workspace is on {workspace.device}, the other tensors on {on.device}")
     if workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes, got {workspace.numel()}")
     return workspace
@@ -607,6 +616,7 @@ def lb_embedding_forward(ids: torch.Tensor, table: torch.Tensor, scale: float = 
     if table.dim() != 2:
         raise ValueError("table must be [V, D]")
     V, D = table.shape
+    _sizes("V D", V, D)
     dtype = table.dtype if dtype is None else dtype
     with _On(stream, (ids, table), ("ids", "table")) as on:
         out = table.new_empty((*ids.shape, D), dtype=dtype)
@@ -629,6 +639,7 @@ def lb_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, scale: 
     if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
         raise ValueError("dout must be [*ids.shape, D]")
     M, D = ids.numel(), dout.shape[-1]
+    _sizes("V D", V, D)
     with _On(stream, (ids, dout), ("ids", "dout")) as on:
         dtable = torch.empty((V, D), dtype=dtype, device=on.device)
         ws = _workspace(workspace, lb_embedding_backward_workspace_bytes(M, V, D), on)
@@ -651,6 +662,7 @@ def _loss_shapes(H, W, labels):
     if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
         raise ValueError("H must be [M, D] and W [V, D]")
     _numel(labels, H.shape[0], "labels")
+    _sizes("M D V", *H.shape, W.shape[0])
     return H.shape[0], H.shape[1], W.shape[0]
 
 
@@ -676,6 +688,7 @@ def lb_cross_entropy_gradient(H: torch.Tensor, W: torch.Tensor, labels: torch.Te
     ``rows``: rows taken at a time (0: 8192), which bounds the workspace."""
     M, D, V = _loss_shapes(H, W, labels)
     _numel(weight, M, "weight")
+    _sizes("rows", rows)
     with _On(stream, (H, W, labels, weight), ("H", "W", "labels", "weight")) as on:
         loss = torch.empty(M, dtype=torch.float32, device=on.device)
         dH = torch.empty((M, D), dtype=torch.bfloat16, device=on.device)
@@ -707,6 +720,8 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
     for i, shape in enumerate(shapes):
         if len(shape) != 2 or 0 in shape:
             raise ValueError(f"G[{i}] must be a matrix with at least one element")
+        if max(shape) >= 1 << 31:
+            raise ValueError(f"G[{i}] has a side of {max(shape)}, 2^31 - 1 at most")
     dtype, names = G[0].dtype, _Names("G")
     code = _element(dtype, "G")
     ints, ptrs = _array(_i, n), _array(_vp, n)

@@ -123,6 +123,27 @@ def test_binding_refuses(lib):
         lib.lb_orthogonalise([torch.zeros(3, 4)])
 
 
+def test_binding_refuses_sizes_past_a_c_int(lib):
+    """ctypes would cut them to 32 bits: a matrix of 2^32 + 16 rows would be taken for one of 16."""
+    huge = (1 << 32) + 16
+    wide = lambda n, m, dtype=torch.float32: torch.zeros(1, 1, dtype=dtype).expand(n, m)   # no memory behind it
+    ids, bf = torch.zeros(3, dtype=torch.int64), torch.bfloat16
+    with pytest.raises(ValueError, match="V must be"):
+        lib.lb_embedding_forward(ids, wide(huge, 8))
+    with pytest.raises(ValueError, match="V must be"):
+        lib.lb_embedding_backward(ids, torch.zeros(3, 8), huge)
+    with pytest.raises(ValueError, match="V must be"):
+        lib.lb_embedding_backward(ids, torch.zeros(3, 8), -1)
+    with pytest.raises(ValueError, match="V must be"):
+        lib.lb_cross_entropy_forward(wide(3, 8, bf), wide(huge, 8, bf), ids)
+    with pytest.raises(ValueError, match="M must be"):
+        lib.lb_cross_entropy_forward(wide(huge, 8, bf), wide(5, 8, bf), ids[:1].expand(huge))
+    with pytest.raises(ValueError, match="rows must be"):
+        lib.lb_cross_entropy_gradient(wide(3, 8, bf), wide(5, 8, bf), ids, torch.zeros(3), rows=huge)
+    with pytest.raises(ValueError, match=r"G\[1\] has a side"):
+        lib.lb_orthogonalise([torch.zeros(3, 4), wide(huge, 16)])
+
+
 @pytest.mark.gpu
 def test_binding_refuses_on_the_gpu(lib):
     ids = torch.zeros(3, dtype=torch.int64, device="cuda")
@@ -137,6 +158,8 @@ def test_binding_refuses_on_the_gpu(lib):
         lib.lb_embedding_forward(ids, table[:, :4])
     with pytest.raises(ValueError, match="workspace must hold"):
         lib.lb_embedding_backward(ids, table[:3], 5, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        lib.lb_embedding_backward(ids, table[:3], 5, workspace=torch.empty(4096, dtype=torch.uint8))
     H, W = torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(5, 8, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(TypeError, match="W must be torch.bfloat16"):
         lib.lb_cross_entropy_forward(H, W.float(), ids)
