@@ -448,6 +448,31 @@ def test_orthogonalise_hard_spectra_of_one_block(lib, kind):
     test_orthogonalise_hard_spectra(lib, 1024, 120, kind)
 
 
+@pytest.mark.parametrize("m,n", [(1 << 24, 2), (1 << 22, 130)])
+def test_orthogonalise_longest(lib, m, n):
+    """The longest sums of squares: a truncating accumulator must not shrink them.  At most 3072 additions of 1.5 * 2^-24
+    scale A_0 by 1 - d, d <= 2.8e-4, and sigma by 1 - d / 2; the result's size then moves by sigma f'(sigma) d / 2 (the
+    rounding to bfloat16 averages out over these many elements)."""
+    a, b, c = 3.4445, -4.7750, 2.0315
+    G = torch.randn(m, n, generator=_gen(m), device="cuda")
+    out, = lib.lb_orthogonalise([G])
+    X = G.double() / G.double().norm()
+    A = X.T @ X
+    lam = torch.linalg.eigvalsh(A)
+    q, dq, l, dl = torch.ones_like(lam), torch.zeros_like(lam), lam, torch.ones_like(lam)
+    one, Q = torch.eye(n, dtype=torch.float64, device="cuda"), torch.eye(n, dtype=torch.float64, device="cuda")
+    for _ in range(5):
+        p = a * one + b * A + c * A @ A
+        Q, A = Q @ p, A @ p @ p
+        f, df = a + b * l + c * l * l, (b + 2 * c * l) * dl
+        q, dq = q * f, dq * f + q * df
+        l, dl = l * f * f, dl * f * f + 2 * l * f * df
+    ref = X @ Q
+    bias = float(((out.double() - ref) * ref).sum() / ref.square().sum())
+    moved = float((1 + 2 * lam * dq / q).abs().max()) * 2.8e-4 / 2
+    assert abs(bias) <= moved + 2.0 ** -15, (bias, moved)
+
+
 def test_orthogonalise_singular_values(lib):
     """What the update is for: five steps bring the singular values of a gradient-like matrix near 1."""
     g = _gen(8)
