@@ -339,9 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
-    // Launched to overlap with the kernel before it (see mm_launch): what follows reads and writes memory that kernel
-    // may still be using, so wait for it to finish; the next kernel may come up as soon as this one has got here.
-    pdl_wait();
+    // Launched to overlap with the kernel before it (see mm_launch), whose memory the copies and the epilogues touch: every
+    // warp waits for its end in its first unit, with what can come before done.
     pdl_go();
 
     if (warp < 4) {
@@ -368,6 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                 const uint32_t bytes[2] = {2 * (kMmOperand + bytes_b), 2 * ((low_a ? kMmOperand : 0) + (low_b ? bytes_b : 0))};
                 const int planes = P.parts > 1 ? 2 : 1, z0 = U.b * (is_a ? P.za : P.zb);
                 const bool low = is_a ? low_a : low_b;
+                if (n == 0) pdl_wait();
                 for (int kb = U.kb0; ok && kb < U.kb1; ++kb)
                     for (int plane = 0; plane < planes; ++plane) {
                         if (!(ok = mbar_wait_warp(&S.empty[s], ph ^ 1, abort, err, 1))) break;
@@ -409,6 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
                     const uint64_t da0 = a_mn ? smem_desc_mn_sw128(S.A[0], kMmSlice) : smem_desc_sw128(S.A[0]);
                     const uint64_t db0 = b_mn ? smem_desc_mn_sw128(S.B[0], kMmSlice) : smem_desc_sw128(S.B[0]);
                     const int chunk = P.chunk, parts = P.parts;
+                    if (n == 0) pdl_wait();   // the bounded waits count from the copies' start
                     const bool low_a = parts == 3 || (parts == 2 && P.b_whole), low_b = parts == 3 || (parts == 2 && !P.b_whole);
                     for (int left = U.kb1 - U.kb0; ok && left > 0; left -= chunk, ++acc) {
                         const int ab = acc & 1;
@@ -477,6 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             T.col0 = U.tn * P.width + side * (P.width / 2);
             T.cols = T.row0 < P.M ? max(0, min(P.width / 2, P.N - T.col0)) : 0;
             typename Epi::State state;
+            if (n == 0) pdl_wait();
             Epi::begin(E, P, U, T, state);
             for (int k0 = U.kb0; k0 < U.kb1; k0 += P.chunk, ++acc) {
                 const int ab = acc & 1;

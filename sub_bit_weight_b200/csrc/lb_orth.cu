@@ -135,6 +135,22 @@ __device__ __forceinline__ void halves(float x, __half &hi, __half &lo)
     lo = __float2half_rn(x - __half2float(hi));
 }
 
+// Two at once, the first in the lower half of a word: half the conversions.
+__device__ __forceinline__ void halves2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __float22half2_rn(x);
+    const float2 back = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x.x - back.x, x.y - back.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+__device__ __forceinline__ float2 sum_of(uint32_t hi, uint32_t lo)
+{
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    return make_float2(h.x + l.x, h.y + l.y);
+}
+
 // X = G scaled to root mean square about 1, as binary16 halves.
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats P)
 {
@@ -375,11 +391,13 @@ struct OrthEpi {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint4 h = lds128(stage(T.st, 0, T.lane, i)), l = lds128(stage(T.st, 1, T.lane, i));
-                const __half *ch = reinterpret_cast<const __half *>(&h), *cl = reinterpret_cast<const __half *>(&l);
+                const uint32_t ch[4] = {h.x, h.y, h.z, h.w}, cl[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[8 * i + j] = fmaf(__uint_as_float(v[8 * i + j]), O.alpha,
-                                        O.beta * (__half2float(ch[j]) + __half2float(cl[j])));
+                for (int j = 0; j < 4; ++j) {
+                    const float2 c2 = sum_of(ch[j], cl[j]);
+                    x[8 * i + 2 * j] = fmaf(__uint_as_float(v[8 * i + 2 * j]), O.alpha, O.beta * c2.x);
+                    x[8 * i + 2 * j + 1] = fmaf(__uint_as_float(v[8 * i + 2 * j + 1]), O.alpha, O.beta * c2.y);
+                }
             }
             put(x, O.D + (size_t)U.b * 2 * plane, plane, O.pn, T, col0, P.N);
             if (O.D2) {
@@ -395,13 +413,7 @@ struct OrthEpi {
     {
         uint32_t w[2][16];   // the row's halves, two to a word
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            __half h0, l0, h1, l1;
-            halves(x[2 * i], h0, l0);
-            halves(x[2 * i + 1], h1, l1);
-            w[0][i] = (uint32_t)__half_as_ushort(h0) | (uint32_t)__half_as_ushort(h1) << 16;
-            w[1][i] = (uint32_t)__half_as_ushort(l0) | (uint32_t)__half_as_ushort(l1) << 16;
-        }
+        for (int i = 0; i < 16; ++i) halves2(make_float2(x[2 * i], x[2 * i + 1]), w[0][i], w[1][i]);
         // the transpose
         __syncwarp();
 #pragma unroll
@@ -710,19 +722,14 @@ __device__ __noinline__ void mid_block(uint32_t acc, uint32_t C, uint32_t D, int
         uint32_t oh[4], ol[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 fh = __half22float2(*reinterpret_cast<const __half2 *>(&ch[j]));
-            const float2 fl = __half22float2(*reinterpret_cast<const __half2 *>(&cl[j]));
-            float2 x = make_float2(fmaf(__uint_as_float(v[8 * i + 2 * j]), alpha, beta * (fh.x + fl.x)),
-                                   fmaf(__uint_as_float(v[8 * i + 2 * j + 1]), alpha, beta * (fh.y + fl.y)));
+            const float2 c2 = sum_of(ch[j], cl[j]);
+            float2 x = make_float2(fmaf(__uint_as_float(v[8 * i + 2 * j]), alpha, beta * c2.x),
+                                   fmaf(__uint_as_float(v[8 * i + 2 * j + 1]), alpha, beta * c2.y));
             if (kDiag) {
                 x.x += c0 + 2 * j == row ? diagonal : 0.0f;
                 x.y += c0 + 2 * j + 1 == row ? diagonal : 0.0f;
             }
-            const __half2 hi = __float22half2_rn(x);
-            const float2 back = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn(x.x - back.x, x.y - back.y);
-            oh[j] = *reinterpret_cast<const uint32_t *>(&hi);
-            ol[j] = *reinterpret_cast<const uint32_t *>(&lo);
+            halves2(x, oh[j], ol[j]);
         }
         if (kDiag) {
             __syncwarp();   // a lane's mirrors are in the others' rows
