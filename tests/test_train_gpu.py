@@ -608,6 +608,35 @@ def test_two_streams_at_once(lib):
     assert all(torch.equal(a, b) for out in out2 for a, b in zip(want2, out))
 
 
+def test_updates_of_every_kind_at_once(lib):
+    """Matrices whose n x n part runs in one block (both ways), in a launch a product, or whole in one block, from two
+    streams and a replayed graph that overlap, the same matrix twice in a list among them."""
+    g = _gen(21)
+    sets = [[torch.randn(s, generator=g, device="cuda") for s in shapes]
+            for shapes in ([(700, 100), (90, 400), (300, 20), (900, 50), (600, 300)], [(256, 128)] * 3 + [(1500, 70), (400, 200)])]
+    for G in sets:
+        G.append(G[0])
+    want = [[t.clone() for t in lib.lb_orthogonalise(G)] for G in sets]
+    for W in want:
+        assert torch.equal(W[0], W[-1])
+    graph, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        held = lib.lb_orthogonalise(sets[0])
+    torch.cuda.synchronize()
+    live, replayed = [], []
+    for _ in range(4):
+        with torch.cuda.stream(other):
+            graph.replay()
+            replayed.append([t.clone() for t in held])
+        live.append((lib.lb_orthogonalise(sets[1], stream=side), lib.lb_orthogonalise(sets[0])))
+    torch.cuda.synchronize()
+    for out in replayed:
+        assert all(torch.equal(a, b) for a, b in zip(want[0], out))
+    for a, b in live:
+        assert all(torch.equal(x, y) for x, y in zip(want[1] + want[0], a + b))
+    assert lib.lb_train_status() == lib.LB_OK
+
+
 def test_a_training_step(lib):
     """The operators as a step of a small model uses them: embedding, a LittleBit layer, the loss over the vocabulary with
     its gradients, back through the layer, the embedding's gradient, and orthogonalised updates of the latent factors;
