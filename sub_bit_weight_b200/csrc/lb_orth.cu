@@ -1124,7 +1124,7 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             return (long)mm_tiles(nt, nt, true, kMmTile) * g.batch;
         };
         auto cut = [&](const Group &g, long unit) {   // as mm_plan cuts
-            // no range above 256 blocks: the accumulator truncates, and 3072 additions lose up to 2.8e-4 of a sum of squares
+            // no range above 256 blocks: the accumulator truncates, and 3 * 1024 additions lose up to 2.8e-4 of a sum of squares
             const long k = blocks(g), most = std::max(64L, (k + 255) / 256);
             const long r = std::min(most, std::max((k + 255) / 256, (k * parts + unit - 1) / unit)), per = (k + r - 1) / r;
             return (k + per - 1) / per;

@@ -450,7 +450,7 @@ def test_orthogonalise_hard_spectra_of_one_block(lib, kind):
 
 @pytest.mark.parametrize("m,n", [(1 << 24, 2), (1 << 22, 130)])
 def test_orthogonalise_longest(lib, m, n):
-    """The longest sums of squares: a truncating accumulator must not shrink them.  At most 3072 additions of 1.5 * 2^-24
+    """The longest sums of squares: a truncating accumulator must not shrink them.  At most 3 * 1024 additions of 1.5 * 2^-24
     scale A_0 by 1 - d, d <= 2.8e-4, and sigma by 1 - d / 2; the result's size then moves by sigma f'(sigma) d / 2 (the
     rounding to bfloat16 averages out over these many elements)."""
     a, b, c = 3.4445, -4.7750, 2.0315
