@@ -107,7 +107,7 @@ LB_API lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W,
  * Orthogonalised updates, for the gradients of latent factors (dU, dV of
  * lb_layer_backward, or their running mean): for each matrix, by the
  * Newton-Schulz iteration of the Muon optimiser,
- *     X = G / (|G|_F + eps);   `steps` times:  
+ *     X = G / (|G|_F + eps);   `steps` times:
  *     X <- a X + b (X X^T) X + c (X X^T)^2 X,   (a, b, c) = (3.4445, -4.7750, 2.0315)
  * which carries every singular value that is not tiny close to 1.
  *
@@ -118,10 +118,11 @@ LB_API lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W,
  * n = 0 is a valid empty call; all matrices of a call share its launches, so
  * pass a block's latents together.  Float32 in effect: products take operands
  * of 22 bits and accumulate in float32, the result is rounded once.  (The
- * iteration runs on G^T G / |G|_F^2: a singular value s |G|_F has there a relative
- * error of about 2^-22 / s^2, which shows for s < 1e-3 after more than five
- * steps, when such values too come close to 1.)  A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN throughout,
- * and touches no other matrix.
+ * iteration runs on G^T G / |G|_F^2: a singular value s |G|_F has there a
+ * relative error of about 2^-22 / s^2, which shows for s < 1e-3 after more than
+ * five steps, when such values too come close to 1.)  A matrix of zeros gives
+ * zeros; one with a NaN or an infinity gives NaN throughout, and touches no
+ * other matrix.
  * Errors: LB_ERR_INVALID_ARG, LB_ERR_UNSUPPORTED (steps > 10, min(rows, cols)
  * > LB_MAX_RANK, a side above 2^24), LB_ERR_OOM (host memory), LB_ERR_CUDA.
  */
