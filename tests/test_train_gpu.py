@@ -619,6 +619,11 @@ def test_updates_of_every_kind_at_once(lib):
     want = [[t.clone() for t in lib.lb_orthogonalise(G)] for G in sets]
     for W in want:
         assert torch.equal(W[0], W[-1])
+    # results of equal shapes may share a storage, never an element, and each is contiguous
+    apart = lib.lb_orthogonalise(sets[1] + [torch.ones(3, 5, device="cuda")] * 2)
+    assert all(t.is_contiguous() for t in apart)
+    ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * 2) for t in apart)
+    assert all(a[1] <= b[0] for a, b in zip(ends, ends[1:]))
     graph, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
     with torch.cuda.graph(graph):
         held = lib.lb_orthogonalise(sets[0])
