@@ -51,6 +51,8 @@
 #pragma once
 
 #include <algorithm>
+#include <utility>
+#include <vector>
 
 #include "lb_internal.cuh"
 #include "lb_tc.cuh"
@@ -90,6 +92,14 @@ struct MmProb {
     int unit0;            // first unit of this problem
 };
 
+// Units by round and pair (kMmNone: the pair has no more), for a launch of few units of different lengths; see mm_deal.
+constexpr int kMmMostDealt = 1024, kMmMostRounds = 16;
+constexpr uint16_t kMmNone = 0xffff;
+struct MmOrder {
+    int n;                // entries, a multiple of the pairs; 0: units are dealt in order
+    uint16_t unit[kMmMostDealt];
+};
+
 template <int kMaxProbs>
 struct MmSmem {
     alignas(1024) unsigned char A[kMmStages][kMmOperand];
@@ -98,6 +108,8 @@ struct MmSmem {
     uint64_t full[kMmStages], empty[kMmStages];
     uint64_t accf[2], acce[2];
     MmProb p[kMaxProbs];   // the launch's records: parameters are read from far away, one latency after another
+    uint16_t dealt[kMmMostRounds];   // this pair's units, where they are dealt by MmBatch::order
+    int ordered;
     uint32_t tmem_base;
     int abort;
 };
@@ -229,13 +241,19 @@ struct MmBatch {
     MmProb p[kMaxProbs];
     int n, nunits;
     int extra;            // see mm_nth
+    MmOrder order;
 };
 
 // The k-th unit of a pair, -1 after its last.  Units are dealt in order, except that where a first problem of long units
 // leaves some pairs one short, those pairs first take `extra` units each of what follows, which fills the gap.
 template <int kMaxProbs>
-__device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, const MmProb *p, int pair, int npairs, int k)
+__device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, const MmSmem<kMaxProbs> &S, int pair, int npairs, int k)
 {
+    if (S.ordered) {
+        const int u = k < kMmMostRounds ? S.dealt[k] : kMmNone;
+        return u == kMmNone ? -1 : u;
+    }
+    const MmProb *const p = S.p;
     if (G.extra == 0) {
         const int u = pair + k * npairs;
         return u < G.nunits ? u : -1;
@@ -253,7 +271,7 @@ __device__ __forceinline__ int mm_nth(const MmBatch<kMaxProbs> &G, const MmProb 
     return u < G.nunits ? u : -1;
 }
 
-__device__ __forceinline__ MmUnit mm_unit(const MmProb *p, int nprobs, int u)
+__host__ __device__ __forceinline__ MmUnit mm_unit(const MmProb *p, int nprobs, int u)
 {
     MmUnit r;
     r.q = 0;
@@ -280,9 +298,10 @@ __device__ __forceinline__ MmUnit mm_unit(const MmProb *p, int nprobs, int u)
         r.tm = local / P.ntn;
         r.tn = local - r.tm * P.ntn;
     }
-    r.half = min(P.width, (P.N - r.tn * P.width + 31) & ~31) >> 1;
+    const int columns = (P.N - r.tn * P.width + 31) & ~31;
+    r.half = (columns < P.width ? columns : P.width) >> 1;
     r.kb0 = r.split * P.kb_per;
-    r.kb1 = min(P.nkb, r.kb0 + P.kb_per);
+    r.kb1 = r.kb0 + P.kb_per < P.nkb ? r.kb0 + P.kb_per : P.nkb;
     return r;
 }
 
@@ -314,6 +333,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 
     for (int i = threadIdx.x; i < nprobs * (int)(sizeof(MmProb) / 4); i += kMmThreads)
         reinterpret_cast<int *>(S.p)[i] = reinterpret_cast<const int *>(G.p)[i];
+    if (threadIdx.x < kMmMostRounds) {
+        const int i = pair + threadIdx.x * npairs;
+        S.dealt[threadIdx.x] = i < G.order.n ? G.order.unit[i] : kMmNone;
+        S.ordered = G.order.n;
+    }
     if (warp == 3 && lane < nprobs) {
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(&G.mA[lane]) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(&G.mB[lane]) : "memory");
@@ -354,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             const uint32_t full0 = map_rank(smem_u32(&S.full[0]), 0);
             uint32_t s = 0, ph = 0;
             bool ok = true;
-            for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0; ++n) {
+            for (int n = 0, u; ok && (u = mm_nth(G, S, pair, npairs, n)) >= 0; ++n) {
                 const MmUnit U = mm_unit(S.p, nprobs, u);
                 const MmProb &P = S.p[U.q];
                 const CUtensorMap *const map = is_a ? &G.mA[U.q] : &G.mB[U.q];
@@ -399,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
             if (rank == 0) {
                 uint32_t s = 0, ph = 0, acc = 0;   // stage, its phase, accumulators used
                 bool ok = true;
-                for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0; ++n) {
+                for (int n = 0, u; ok && (u = mm_nth(G, S, pair, npairs, n)) >= 0; ++n) {
                     const MmUnit U = mm_unit(S.p, nprobs, u);
                     const MmProb &P = S.p[U.q];
                     const bool a_mn = P.a_mn != 0, b_mn = P.b_mn != 0;
@@ -471,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
         MmTileCtx T;
         T.lane = lane;
         T.st = smem_u32(S.ST[warp - 4]);
-        for (int n = 0, u; ok && (u = mm_nth(G, S.p, pair, npairs, n)) >= 0 && !*abort; ++n) {
+        for (int n = 0, u; ok && (u = mm_nth(G, S, pair, npairs, n)) >= 0 && !*abort; ++n) {
             const MmUnit U = mm_unit(S.p, nprobs, u);
             const MmProb &P = S.p[U.q];
             T.row0 = U.tm * kMmTile + (int)rank * kMmHalf + q4 * 32;
@@ -549,6 +573,40 @@ inline cudaError_t mm_pairs(int *pairs)
     const cudaError_t e = sm_count_of_current(&sms);
     *pairs = sms / 2 > 0 ? sms / 2 : 1;
     return e;
+}
+// Host: deal the units of a launch to its pairs, the longest first, each to the pair with least to do.  A k block of a unit
+// takes the tensor cores 512 cycles for each product of whole tiles, or its copies at about 42 bytes a cycle, which a tile
+// of few columns waits for.  For launches of few units of different lengths; where they are equal this is their order.  Of 28 matrices of ranks 800 and 544 (216 units of
+// 9 or 13 k blocks) the first pair ended after 16 us and the last after 52 in order, and after 35 and 42 so.
+inline void mm_deal(MmOrder &O, const MmProb *p, int nprobs, int nunits, int pairs)
+{
+    O.n = 0;
+    if (nunits <= pairs || nunits > kMmMostDealt) return;
+    std::vector<std::pair<long, int>> units(nunits);   // (-cost, unit)
+    for (int u = 0; u < nunits; ++u) {
+        const MmUnit U = mm_unit(p, nprobs, u);
+        const MmProb &P = p[U.q];
+        const long planes = P.parts > 1 ? 2 : 1;
+        const long products = 512L * P.parts * U.half / kMmHalf, copies = planes * (kMmHalf + U.half) * kMmBK * 2 / 42;
+        units[u] = {-(U.kb1 - U.kb0) * std::max(products, copies) - 1000, u};
+    }
+    std::sort(units.begin(), units.end());
+    std::vector<std::pair<long, int>> load(pairs);     // a heap: (-what a pair has to do, pair)
+    std::vector<int> taken(pairs, 0);
+    for (int i = 0; i < pairs; ++i) load[i] = {0, -i};
+    for (uint16_t &u : O.unit) u = kMmNone;
+    int rounds = 0;
+    for (const auto &[cost, u] : units) {
+        std::pop_heap(load.begin(), load.end());
+        auto &[left, pair] = load.back();
+        const int at = taken[-pair]++ * pairs - pair;
+        if (at >= kMmMostDealt || taken[-pair] > kMmMostRounds) return;
+        O.unit[at] = (uint16_t)u;
+        rounds = std::max(rounds, taken[-pair]);
+        left += cost;
+        std::push_heap(load.begin(), load.end());
+    }
+    O.n = std::min(rounds * pairs, kMmMostDealt);
 }
 inline int mm_units(const MmProb &P) { return P.tiles * P.batch * P.splits; }
 

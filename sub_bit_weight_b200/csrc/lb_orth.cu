@@ -1237,6 +1237,12 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     const int wq = width_of(square_tiles), wo = width_of(update_tiles);
     bool ok = true;
     auto begin = [&]() { memset(&B, 0, sizeof(B)); };
+    MmOrder one, two;   // of the launches with one product of each matrix, and with two
+    one.n = two.n = -1;
+    auto deal = [&](MmOrder &O) {
+        if (O.n < 0) mm_deal(O, B.p, B.n, B.nunits, pairs);
+        B.order = O;
+    };
     auto launch = [&]() -> cudaError_t {
         if (B.n == 0) return cudaSuccess;
         ++*launches;
@@ -1259,6 +1265,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         B.nunits += mm_units(P);
         ++B.n;
     }
+    mm_deal(B.order, B.p, B.n, B.nunits, pairs);
     if (!ok) return LB_ERR_INVALID_ARG;
     if ((e = launch()) != cudaSuccess) return status_from(e);
 
@@ -1335,6 +1342,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
                 O.gamma = kA * kSA;
             }
         }
+        deal(one);
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
         if (k + 1 == steps && k == 0) break;
@@ -1348,12 +1356,14 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
                 square(g, from, g.q, to, f / kSA, kA * f, from);
             }
         }
+        deal(k && k + 1 < steps ? two : one);
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
         if (k + 1 == steps) break;
         begin();   // A <- a T + T p
         for (const Group &g : C.groups)
             if (g.n > kMidN) square(g, g.T, g.q, g.A, 1.0f / kSA, kA, g.T);
+        deal(one);
         if (!ok) return LB_ERR_INVALID_ARG;
         if ((e = launch()) != cudaSuccess) return status_from(e);
     }
@@ -1382,6 +1392,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         B.nunits += mm_units(P);
         ++B.n;
     }
+    mm_deal(B.order, B.p, B.n, B.nunits, pairs);
     if (!ok) return LB_ERR_INVALID_ARG;
     if ((e = launch()) != cudaSuccess) return status_from(e);
     return status_from(cudaGetLastError());
