@@ -574,10 +574,11 @@ inline cudaError_t mm_pairs(int *pairs)
     *pairs = sms / 2 > 0 ? sms / 2 : 1;
     return e;
 }
-// Host: deal the units of a launch to its pairs, the longest first, each to the pair with least to do.  A k block of a unit
-// takes the tensor cores 512 cycles for each product of whole tiles, or its copies at about 42 bytes a cycle, which a tile
-// of few columns waits for.  For launches of few units of different lengths; where they are equal this is their order.  Of 28 matrices of ranks 800 and 544 (216 units of
-// 9 or 13 k blocks) the first pair ended after 16 us and the last after 52 in order, and after 35 and 42 so.
+// Host: deal the units of a launch to its pairs, the longest first, each to the pair with least to do: for launches of few
+// units of different lengths (where they are equal this is their order).  A k block of a unit takes the tensor cores 512
+// cycles for each product of whole tiles, or its copies at about 42 bytes a cycle, which a tile of few columns waits for.
+// Of 28 matrices of ranks 800 and 544 (216 units of 9 or 13 k blocks) the first pair ended after 16 us and the last after
+// 52 in order, and after 35 and 42 so.
 inline void mm_deal(MmOrder &O, const MmProb *p, int nprobs, int nunits, int pairs)
 {
     O.n = 0;
