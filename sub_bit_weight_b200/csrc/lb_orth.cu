@@ -49,7 +49,8 @@
 //
 // Copied once, the four halves of 64 k of a tile are 64 KB for three products'
 // 1536 cycles of the tensor cores (copied for each product they would be 96):
-// about 60 us a launch for 28 matrices (12 of rank 800, 16 of rank 544).
+// 51 us a launch for 28 matrices (12 of rank 800, 16 of rank 544), 96 where
+// there are two products of each.
 
 #include <algorithm>
 #include <cmath>
