@@ -20,7 +20,8 @@
  * and mean nothing afterwards.  Calls that use different workspaces and
  * outputs may overlap on the device (streams, captured graphs); calls that
  * share one must be ordered.  All calls can be captured into a CUDA graph.
- * Outputs must not overlap inputs.  Results are the same bits in every run.
+ * Outputs must not overlap inputs.  The same call gives the same bits every
+ * time.
  */
 #ifndef LITTLEBIT_TRAIN_H
 #define LITTLEBIT_TRAIN_H
@@ -116,7 +117,9 @@ LB_API lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t *W,
  *   steps  1 .. 10 (5 is usual);  eps >= 0 (1e-7 is usual)
  *   O      [n] pointers to bfloat16 [rows_i][cols_i], overwritten
  * n = 0 is a valid empty call; all matrices of a call share its launches, so
- * pass a block's latents together.  Float32 in effect: products take operands
+ * pass a block's latents together.  (They also share the GPU: how the sum over a
+ * long axis is cut follows from the whole set, so a matrix's last float32 bits
+ * may depend on what else is in the call.)  Float32 in effect: products take operands
  * of 22 bits and accumulate in float32, the result is rounded once.  (The
  * iteration runs on G^T G / |G|_F^2: a singular value s |G|_F has there a
  * relative error of about 2^-22 / s^2, which shows for s < 1e-3 after more than

@@ -561,13 +561,6 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
 
 bool misaligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
-// accumulators of equal lengths, at most kChunk k blocks
-void set_chunk(MmProb &P)
-{
-    const int chunks = (P.kb_per + kChunk - 1) / kChunk;
-    P.chunk = (P.kb_per + chunks - 1) / chunks;
-}
-
 lb_status few_logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, int M, int D, int V, unsigned char *ws,
                      cudaStream_t s)
 {
@@ -577,7 +570,7 @@ lb_status few_logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, in
     const int width = M <= 64 ? 64 : 128;
     G.n = 1;
     mm_plan(G.p[0], V, M, D, true, 0, L.ranges, 1, 1, false, width);
-    set_chunk(G.p[0]);
+    mm_chunk(G.p[0], kChunk);
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.mA[0], true, false, W, V, D, D) ||
         !mm_operand(&G.mB[0], true, false, H, M, D, D, 1, width / 2) ||
@@ -594,7 +587,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     memset(&G, 0, sizeof(G));
     G.n = 1;
     mm_plan(G.p[0], M, V, D, true, 0, 1);
-    set_chunk(G.p[0]);
+    mm_chunk(G.p[0], kChunk);
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.mA[0], true, false, H, M, D, D) || !mm_operand(&G.mB[0], true, false, W, V, D, D))
         return LB_ERR_INVALID_ARG;

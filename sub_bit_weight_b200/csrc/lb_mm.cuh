@@ -566,6 +566,12 @@ inline void mm_plan(MmProb &P, int M, int N, long K, bool m_fast, int unit0, int
     P.kb_per = (P.nkb + splits - 1) / splits;
     P.splits = (P.nkb + P.kb_per - 1) / P.kb_per;
 }
+// Host: accumulators of equal lengths, at most `most` k blocks, which the epilogue adds.
+inline void mm_chunk(MmProb &P, int most)
+{
+    const int chunks = (P.kb_per + most - 1) / most;
+    P.chunk = (P.kb_per + chunks - 1) / chunks;
+}
 // Host: CTA pairs that run at once on the current device.
 inline cudaError_t mm_pairs(int *pairs)
 {

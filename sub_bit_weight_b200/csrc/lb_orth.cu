@@ -23,10 +23,12 @@
 // product is hi hi + lo hi + hi lo in one float32 accumulator for each k block,
 // whose halves are copied once for the three.  p is kept rather than q, whose
 // diagonal would round by a 2^-23, and the products are made exactly symmetric.
+// A_0's sums over the long axis are taken in short pieces (GramEpi).
 // Measured against binary64, as parts of the result's norm: 1.7e-3, which is the
 // rounding to bfloat16, for Gaussian and gradient-like matrices; at most 2.2e-3
 // for spectra that fall off by 1e4 or have one dominant value (plain bfloat16
-// iterations: 2e-2 to 2e-1).  That is after five steps; singular values below
+// iterations: 2e-2 to 2e-1), and the same whatever else is in the call.  That is
+// after five steps; singular values below
 // some 1e-3 of the norm, lifted to 1 by up to ten steps, come out with relative
 // errors of about 2^-22 over their square (1e-2 of the norm for a square Gaussian
 // matrix of rank 65 that has one).  Scales are powers of two that keep the halves clear
@@ -69,6 +71,8 @@ constexpr int kNormBlocks = 592;                 // blocks (and partial sums) a 
 constexpr int kSmallN = 64;
 constexpr float kSA = 8192.0f;                   // scale of A, p and T
 constexpr int kMaxSteps = 10;
+// k blocks of A_0 one accumulator takes, divided by the products of halves: 60 or 64 additions (see GramEpi).
+constexpr int kGramChunk = 16;
 
 // One matrix as the elementwise kernels see it.
 struct Mat {
@@ -217,10 +221,62 @@ __device__ __forceinline__ uint32_t pack_bf(uint32_t a, uint32_t b, float f)
 }
 
 // ---- products
-enum { kPart = 0, kSym = 1, kOut = 2 };
+// A_0: the partial sums of each k range.  The accumulator truncates, and what 2064 additions over 11008 rows lose of A_0
+// (up to 9e-5, unevenly) moved small singular values until results were off by 4.5e-3 (1/j^2 spectrum, 800 columns) where
+// their rounding is 1.7e-3; so it takes 320 or 1024 rows at a time, and these pieces are added in registers: 1.73e-3, at no
+// measurable time (6 of 11008 x 800: 763 -> 766 us a call, the 28 of a block 1695 -> 1695).
+struct GramEpi {
+    static constexpr bool kManyRegs = true;
+    struct Params {
+        CUtensorMap mD[kMostGroups];   // float32 [ranges * batch][n][pn]
+    };
+    struct State {
+        float a[kMmHalf];
+    };
+    static __device__ __forceinline__ void begin(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &S)
+    {
+#pragma unroll
+        for (int i = 0; i < kMmHalf; ++i) S.a[i] = 0.0f;   // taking the first piece as it is spilled registers
+    }
+    static __device__ __forceinline__ void take(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &T, State &S,
+                                                bool, bool, bool &)
+    {
+        if (T.cols == 0) return;
+#pragma unroll
+        for (int c = 0; c < kMmHalf; c += 32) {   // columns past the last one hold anything and go nowhere
+            uint32_t v[32];
+            tmem_ld32(T.tmem + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S.a[c + i] += __uint_as_float(v[i]);
+        }
+    }
+    static __device__ __forceinline__ void end(const Params &E, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
+                                               State &S, bool &stored)
+    {
+#pragma unroll
+        for (int c = 0; c < kMmHalf; c += 32) {
+            if (c >= T.cols) continue;
+            if (stored) {
+                if (T.lane == 0) tma_store_wait_read();
+                __syncwarp();
+            }
+            stored = true;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *a = S.a + c + 4 * i;
+                sts128(T.st + sw128(T.lane, i), make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]),
+                                                           __float_as_uint(a[2]), __float_as_uint(a[3])));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (T.lane == 0) tma_store_3d(&E.mD[U.q], T.col0 + c, T.row0, U.split * P.batch + U.b, T.st);
+        }
+    }
+};
+
+enum { kSym = 0, kOut = 1 };
 constexpr int kMostProbs = 2 * kMostGroups;
 struct OrthProb {
-    CUtensorMap mD;       // kPart: float32 [ranges * batch][n][pn]
     int kind;
     int pn;               // row pitch of the n x n arrays
     int first;            // index of the batch's first matrix
@@ -289,29 +345,11 @@ struct OrthEpi {
     {
     }
     static __device__ __forceinline__ void take(const Params &E, const MmProb &P, const MmUnit &U, const MmTileCtx &T,
-                                                State &S, bool, bool, bool &stored)
+                                                State &S, bool, bool, bool &)
     {
         const OrthProb &O = E.p[U.q];
         const int row = T.row0 + T.lane;
         uint32_t v[32];
-        if (O.kind == kPart) {
-            const int z = U.split * P.batch + U.b;
-            for (int c = 0; c < T.cols; c += 32) {
-                tmem_ld32(T.tmem + c, v);
-                if (stored) {
-                    if (T.lane == 0) tma_store_wait_read();
-                    __syncwarp();
-                }
-                stored = true;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sts128(T.st + sw128(T.lane, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-                fence_proxy_async();
-                __syncwarp();
-                if (T.lane == 0) tma_store_3d(&O.mD, T.col0 + c, T.row0, z, T.st);
-            }
-            return;
-        }
         if (O.kind == kOut) {
             if (T.cols == 0) return;
             uint16_t *const base = E.out[O.first + U.b];
@@ -1125,7 +1163,7 @@ void orth_chunks(std::vector<Chunk> &out, const int *rows, const int *cols, int 
             return (long)mm_tiles(nt, nt, true, kMmTile) * g.batch;
         };
         auto cut = [&](const Group &g, long unit) {   // as mm_plan cuts
-            // no range above 256 blocks: the accumulator truncates, and 3 * 1024 additions lose up to 2.8e-4 of a sum of squares
+            // no range above 256 blocks, some 50 of the pieces that are added in a row
             const long k = blocks(g), most = std::max(64L, (k + 255) / 256);
             const long r = std::min(most, std::max((k + 255) / 256, (k * parts + unit - 1) / unit)), per = (k + r - 1) / r;
             return (k + per - 1) / per;
@@ -1251,24 +1289,26 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
     };
 
     // A_0: both operands are X, contracted over the long axis
-    begin();
+    MmBatch<kMostGroups> R;
+    GramEpi::Params D;
+    memset(&R, 0, sizeof(R));
     for (const Group &g : C.groups) {
-        MmProb &P = B.p[B.n];
-        OrthProb &O = E.p[B.n];
-        mm_plan(P, g.n, g.n, g.m, false, B.nunits, g.ranges, parts, g.batch, true);
+        MmProb &P = R.p[R.n];
+        mm_plan(P, g.n, g.n, g.m, false, R.nunits, g.ranges, parts, g.batch, true);
+        mm_chunk(P, kGramChunk / parts);
         P.a_mn = P.b_mn = g.wide ? 0 : 1;
         P.za = P.zb = xz;
-        ok = ok && mm_operand(&B.mA[B.n], false, P.a_mn, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
-        B.mB[B.n] = B.mA[B.n];
-        O.kind = kPart;
-        ok = ok && tmap_encode_3d(&O.mD, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + g.part, g.pn, g.n,
+        ok = ok && mm_operand(&R.mA[R.n], false, P.a_mn, ws + g.X, g.rows, g.cols, g.pitch, (long)g.batch * xz);
+        R.mB[R.n] = R.mA[R.n];
+        ok = ok && tmap_encode_3d(&D.mD[R.n], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + g.part, g.pn, g.n,
                                   (long)g.ranges * g.batch, (long)g.pn * 4, (long)g.n * g.pn * 4, 32, 32);
-        B.nunits += mm_units(P);
-        ++B.n;
+        R.nunits += mm_units(P);
+        ++R.n;
     }
-    mm_deal(B.order, B.p, B.n, B.nunits, pairs);
+    mm_deal(R.order, R.p, R.n, R.nunits, pairs);
     if (!ok) return LB_ERR_INVALID_ARG;
-    if ((e = launch()) != cudaSuccess) return status_from(e);
+    ++*launches;
+    if ((e = mm_launch<false, kMostGroups, GramEpi>(R, D, s)) != cudaSuccess) return status_from(e);
 
     // the small ranks' polynomials, the others' A_0
     Groups big, mid, small;
