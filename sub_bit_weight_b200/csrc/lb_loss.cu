@@ -35,7 +35,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kEScale = 15.0f;        // e is stored times 2^15
-constexpr int kChunk = 16;             // k blocks (1024 k) of logits one accumulator takes, see lb_mm.cuh
+constexpr int kChunk = 16;             // k blocks (1024 k) one accumulator takes, see lb_mm.cuh
 constexpr int kGradCols = 8192;         // entries of a row one block of the second step takes, or up to four times that
 constexpr int kRowsDefault = 8192, kRowsMost = 32768;
 
@@ -382,60 +382,75 @@ __global__ void __launch_bounds__(256) grad_kernel(uint4 *__restrict__ E, const 
 }
 
 // ---- 3: the two products
+// Their sums run over the whole vocabulary (dH) or all rows of a piece (dW): pieces of an accumulator, as for the logits,
+// are added in registers.  (One accumulator over 131,072 entries of one sign came out up to 1e-3 low.)
 enum { kOutBf16 = 0, kOutF32 = 1, kOutF32Add = 2 };
 struct ProductEpi {
-    static constexpr bool kManyRegs = false;
+    static constexpr bool kManyRegs = true;
     struct Params {
         CUtensorMap mD[2];
         int kind[2];
         int split_rows[2];   // rows between the partial results of consecutive k ranges
         const float *wref;
     };
-    struct State {};
-    static __device__ __forceinline__ void begin(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &)
+    struct State {
+        float a[kMmHalf];
+    };
+    static __device__ __forceinline__ void begin(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &S)
     {
+#pragma unroll
+        for (int i = 0; i < kMmHalf; ++i) S.a[i] = 0.0f;
     }
-    static __device__ __forceinline__ void end(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &, State &,
-                                               bool &)
+    static __device__ __forceinline__ void take(const Params &, const MmProb &, const MmUnit &, const MmTileCtx &T, State &S,
+                                                bool, bool, bool &)
     {
+        if (T.cols == 0) return;
+#pragma unroll
+        for (int c = 0; c < kMmHalf; c += 32) {   // columns past the last one hold anything and go nowhere
+            uint32_t v[32];
+            tmem_ld32(T.tmem + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S.a[c + i] += __uint_as_float(v[i]);
+        }
     }
-    static __device__ __forceinline__ void take(const Params &E, const MmProb &, const MmUnit &U, const MmTileCtx &T,
-                                                State &, bool, bool, bool &stored)
+    static __device__ __forceinline__ void end(const Params &E, const MmProb &, const MmUnit &U, const MmTileCtx &T,
+                                               State &S, bool &stored)
     {
         const int kind = E.kind[U.q], y = T.row0 + U.split * E.split_rows[U.q];
         const CUtensorMap *map = &E.mD[U.q];
-        const float f = kind == kOutBf16 ? *E.wref : 1.0f;
-        uint32_t v[32];
-        for (int c = 0; c < T.cols; c += 32) {
-            tmem_ld32(T.tmem + c, v);
-            if (kind == kOutBf16) {
-                const int half = (c >> 5) & 1;
-                if (half == 0) staging_free(stored, T.lane);
+        if (kind == kOutBf16) {
+            const float f = *E.wref;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        p[j] = pack_bf2(__uint_as_float(v[8 * i + 2 * j]) * f, __uint_as_float(v[8 * i + 2 * j + 1]) * f);
-                    sts128(T.st + sw128(T.lane, half * 4 + i), make_uint4(p[0], p[1], p[2], p[3]));
-                }
-                if (half == 0 && c + 32 < T.cols) continue;
-                fence_proxy_async();
-                __syncwarp();
-                if (T.lane == 0) tma_store_2d(map, T.col0 + (c & ~63), y, T.st);
-            } else {
+            for (int c = 0; c < kMmHalf; c += 64) {
+                if (c >= T.cols) break;
                 staging_free(stored, T.lane);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sts128(T.st + sw128(T.lane, i), make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                for (int i = 0; i < 8; ++i) {
+                    const float *a = S.a + c + 8 * i;
+                    sts128(T.st + sw128(T.lane, i), make_uint4(pack_bf2(a[0] * f, a[1] * f), pack_bf2(a[2] * f, a[3] * f),
+                                                               pack_bf2(a[4] * f, a[5] * f), pack_bf2(a[6] * f, a[7] * f)));
+                }
                 fence_proxy_async();
                 __syncwarp();
-                if (T.lane == 0) {
-                    if (kind == kOutF32)
-                        tma_store_2d(map, T.col0 + c, y, T.st);
-                    else
-                        tma_add_2d(map, T.col0 + c, y, T.st);
-                }
+                if (T.lane == 0) tma_store_2d(map, T.col0 + c, y, T.st);
+            }
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < kMmHalf; c += 32) {
+            if (c >= T.cols) break;
+            staging_free(stored, T.lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float *a = S.a + c + 4 * i;
+                sts128(T.st + sw128(T.lane, i), make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]),
+                                                           __float_as_uint(a[2]), __float_as_uint(a[3])));
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (T.lane == 0) {
+                if (kind == kOutF32) tma_store_2d(map, T.col0 + c, y, T.st);
+                else tma_add_2d(map, T.col0 + c, y, T.st);
             }
         }
     }
@@ -624,6 +639,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     E.wref = (const float *)(ws + L.wref);
     MmProb &P = G.p[0];
     mm_plan(P, M, D, V, true, 0, L.splits);
+    mm_chunk(P, kChunk);
     P.b_mn = 1;
     if (!mm_operand(&G.mA[0], true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[0], true, true, W, V, D, D))
         return LB_ERR_INVALID_ARG;
@@ -644,6 +660,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     if (dW) {
         MmProb &Q = G.p[1];
         mm_plan(Q, V, D, M, false, G.nunits, 1);
+        mm_chunk(Q, kChunk);
         Q.a_mn = Q.b_mn = 1;
         if (!mm_operand(&G.mA[1], true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[1], true, true, ws + L.Hc, M, D, D))
             return LB_ERR_INVALID_ARG;

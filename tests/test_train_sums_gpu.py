@@ -4,7 +4,7 @@ all but cancels, and updates whose small singular values an error of the Gram ma
 import pytest
 import torch
 
-from test_train_gpu import BF16, _gen, _off, _orth_ref, lib  # noqa: F401
+from test_train_gpu import BF16, MMA, _gen, _off, _orth_ref, _within, lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,52 @@ def test_orthogonalise_hard_spectra_of_the_largest_rank(lib, kind):  # noqa: F81
     """The n x n products are longest at rank 2048."""
     hard = _spectrum(_gen(6), 2200, 2048, kind)
     assert _off(lib.lb_orthogonalise([hard])[0], _orth_ref(hard)) <= 2.2e-3
+
+
+# The gradients of the loss where every probability is a power of two (all logits zero), so that G is known to the last bit.
+# Weights of 1 and 255/256 give products finer than the accumulator; nearly all terms have one sign, and the last ones (the
+# label's) cancel the sum, so that a bias of the sum shows beside the rounding of the small result.  Bound: 64 additions of
+# 2^-22 for each 1024 k of the magnitudes there, 2^-24 of the largest sum for each of these pieces added, the rounding.
+
+def _weights(M):
+    return torch.where(torch.arange(M, device="cuda") % 2 == 0, 1.0, 255 / 256)
+
+
+def test_cross_entropy_gradient_of_hidden_states_over_a_long_vocabulary(lib):  # noqa: F811
+    M, D, V = 512, 9472, 1 << 17                                  # 74 tiles: the vocabulary is not cut
+    g = _gen(1)
+    W = torch.empty(V, D, dtype=BF16, device="cuda")
+    for v in range(0, V, 1 << 14):
+        W[v:v + (1 << 14)] = 1 + torch.randint(0, 128, (1 << 14, D), generator=g, device="cuda") / 128
+    W[V - 1] = 1.5
+    H = torch.zeros(M, D, dtype=BF16, device="cuda")
+    labels = torch.full((M,), V - 1, device="cuda")
+    weight = _weights(M)
+    _, dH, _ = lib.lb_cross_entropy_gradient(H, W, labels, weight, head=False)
+    p = weight.double()[:, None] / V
+    at_label = (weight.double() * (1 / V - 1)).to(BF16).double()[:, None]
+    sums = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for v in range(0, V - 1, 1 << 14):
+        sums += W[v:min(v + (1 << 14), V - 1)].sum(0, dtype=torch.float64)
+    ref = p * sums + at_label * 1.5
+    pieces = V // 1024
+    bound = 64 * MMA * (p * sums + 1.5) + pieces * 2.0 ** -24 * 2.0
+    assert float(ref.abs().max()) < 0.02                          # the sum is all but cancelled
+    _within(dH, ref, bound + 2.0 ** -8 * (ref.abs() + bound))
+
+
+def test_cross_entropy_gradient_of_the_vocabulary_over_many_rows(lib):  # noqa: F811
+    M, D, V = 32768, 256, 256
+    g = _gen(2)
+    H = (1.5 + torch.randint(-2, 3, (M, D), generator=g, device="cuda") / 128).to(BF16)
+    W = torch.zeros(V, D, dtype=BF16, device="cuda")
+    labels = torch.arange(M, device="cuda") // 128
+    weight = _weights(M)
+    _, _, dW = lib.lb_cross_entropy_gradient(H, W, labels, weight, rows=M)
+    G = (weight.double() / V)[:, None].expand(M, V).clone()
+    G[torch.arange(M, device="cuda"), labels] = (weight.double() * (1 / V - 1)).to(BF16).double()
+    Hd = H.double()
+    ref = G.T @ Hd
+    mags = torch.stack([G[m:m + 1024].T.abs() @ Hd[m:m + 1024] for m in range(0, M, 1024)])
+    bound = 64 * MMA * mags.sum(0) + len(mags) * 2.0 ** -24 * 200.0
+    _within(dW, ref, bound + 2.0 ** -8 * (ref.abs() + bound))
