@@ -16,8 +16,9 @@
  * anything is enqueued, nothing synchronises the host unless it says so.  No
  * call here allocates device memory or keeps anything between calls: scratch
  * is the `workspace` argument, 256-byte aligned and at least as large as the
- * matching *_workspace_bytes call says; its contents need not be initialised
- * and mean nothing afterwards.  Calls that use different workspaces and
+ * matching *_workspace_bytes call says (host only; 0 also for sizes that the
+ * operator refuses); its contents need not be initialised and mean nothing
+ * afterwards.  Calls that use different workspaces and
  * outputs may overlap on the device (streams, captured graphs); calls that
  * share one must be ordered.  All calls can be captured into a CUDA graph.
  * Outputs must not overlap inputs.  The same call gives the same bits every
@@ -75,8 +76,8 @@ LB_API lb_status lb_embedding_backward(const int64_t *ids, int64_t M, const void
  * and sum of the softmax are float32.  A row with a NaN or an infinite logit
  * has lse and loss NaN (an infinity below every other logit counts as weight 0).
  * Errors: LB_ERR_INVALID_ARG (null, misaligned, bad size, workspace too
- * small), LB_ERR_UNSUPPORTED (D not a multiple of 8, sizes past 2^30 rows or
- * tiles), LB_ERR_CUDA.
+ * small), LB_ERR_UNSUPPORTED (D not a multiple of 8; M or V above 2^28, D above
+ * 2^20, or more than 2^28 tiles of 256 x 256 in a product), LB_ERR_CUDA.
  */
 LB_API size_t lb_cross_entropy_forward_workspace_bytes(int M, int D, int V);
 LB_API lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t *W, const int64_t *labels, int M, int D,

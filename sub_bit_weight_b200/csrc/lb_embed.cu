@@ -311,7 +311,7 @@ struct EmbedPlan {
 
 bool embed_plan(EmbedPlan &L, long long M, int V, int D)
 {
-    if (M < 0 || V < 1 || D < 1 || M > (1LL << 31) - 1) return false;
+    if (M < 0 || V < 1 || D < 1 || M > (1LL << 31) - 1 || D > (1 << 23)) return false;
     const long long c = M ? (M + kSortMost - 1) / kSortMost : 0;
     L.nchunks = (int)c;
     L.chunk = c ? (int)((M + c - 1) / c) : 0;
@@ -447,7 +447,7 @@ extern "C" lb_status lb_embedding_backward(const int64_t *ids, int64_t M, const 
     set_launch_count(0);
     EmbedPlan L;
     if (M < 0 || V < 1 || D < 1 || !known(dout_dtype) || !known(dtable_dtype)) return LB_ERR_INVALID_ARG;
-    if (D > (1 << 23) || !embed_plan(L, M, V, D)) return LB_ERR_UNSUPPORTED;
+    if (!embed_plan(L, M, V, D)) return LB_ERR_UNSUPPORTED;
     const size_t si = size_of(dout_dtype), so = size_of(dtable_dtype);
     if (!dtable || misaligned(dtable, so)) return LB_ERR_INVALID_ARG;
     if (M > 0 && (!ids || !dout || !workspace || misaligned(ids, 8) || misaligned(dout, si) ||

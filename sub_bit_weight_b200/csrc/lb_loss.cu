@@ -538,15 +538,18 @@ struct LossPlan {
     size_t stat, target, wref, E, Hc, part, acc, bytes;   // workspace offsets
 };
 
+// false: sizes that the operators refuse
 bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int rows)
 {
-    if (M < 0 || D < 1 || V < 1 || rows < 0 || D > (1 << 20) || V > (1 << 28) || M > (1 << 28)) return false;
+    if (M < 0 || D < 1 || V < 1 || rows < 0 || D % 8 || D > (1 << 20) || V > (1 << 28) || M > (1 << 28)) return false;
     memset(&L, 0, sizeof(L));
     L.rows = std::min(std::max(M, 1), grad ? (rows ? std::min(rows, kRowsMost) : kRowsDefault) : std::max(M, 1));
     L.npieces = M ? (M + L.rows - 1) / L.rows : 0;
     L.ntn = (V + kMmTile - 1) / kMmTile;
     L.nst = (V + kMmHalf - 1) / kMmHalf;
     L.Vp = (V + 63) & ~63;   // rows of e begin on 128-byte lines: 16 bytes off, every store splits its sectors
+    const size_t tiles_m = (L.rows + kMmTile - 1) / kMmTile, tiles_d = (D + kMmTile - 1) / kMmTile, tiles_n = L.ntn;
+    if (tiles_m * tiles_n > (1u << 28)) return false;   // units of a launch, with its k ranges an int
     size_t at = 0;
     auto take = [&](size_t b) {
         const size_t o = at;
@@ -564,6 +567,7 @@ bool loss_plan(LossPlan &L, int M, int D, int V, bool grad, bool with_dW, int ro
     if (grad) {
         // the plan's pairs: those of the B200's 148 SMs, whatever the current device, so that the size is one number
         L.splits = dh_splits(L.rows, D, V, with_dW, 74);
+        if (tiles_n * tiles_d > (1u << 28) || tiles_m * tiles_d * L.splits > (1u << 28)) return false;
         L.E = take((size_t)L.rows * L.Vp * 2);
         const size_t tile_rows = (size_t)((L.rows + kMmTile - 1) / kMmTile) * kMmTile;
         L.part = take(L.splits > 1 ? (size_t)L.splits * tile_rows * D * 4 : 0);
@@ -723,13 +727,12 @@ extern "C" lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t 
     set_launch_count(0);
     LossPlan L;
     if (M < 0 || D < 1 || V < 1) return LB_ERR_INVALID_ARG;
-    if (D % 8 || !loss_plan(L, M, D, V, false, false, 0)) return LB_ERR_UNSUPPORTED;
+    if (!loss_plan(L, M, D, V, false, false, 0)) return LB_ERR_UNSUPPORTED;
     if (M == 0) return LB_OK;
     if (!H || !W || !labels || !loss || !lse || !workspace) return LB_ERR_INVALID_ARG;
     if (misaligned(H, 16) || misaligned(W, 16) || misaligned(labels, 8) || misaligned(loss, 4) || misaligned(lse, 4) ||
         misaligned(workspace, 256) || workspace_bytes < L.bytes)
         return LB_ERR_INVALID_ARG;
-    if ((size_t)((M + kMmTile - 1) / kMmTile) * L.ntn > (1u << 30)) return LB_ERR_UNSUPPORTED;
     if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
     unsigned char *ws = (unsigned char *)workspace;
     cudaStream_t s = (cudaStream_t)stream;
@@ -757,7 +760,7 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     set_launch_count(0);
     LossPlan L;
     if (M < 0 || D < 1 || V < 1 || rows < 0) return LB_ERR_INVALID_ARG;
-    if (D % 8 || !loss_plan(L, M, D, V, true, dW != nullptr, rows)) return LB_ERR_UNSUPPORTED;
+    if (!loss_plan(L, M, D, V, true, dW != nullptr, rows)) return LB_ERR_UNSUPPORTED;
     if (misaligned(dW, 16)) return LB_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     if (M == 0) {   // no rows: the gradient of W is zero
@@ -768,9 +771,6 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
     if (misaligned(H, 16) || misaligned(W, 16) || misaligned(labels, 8) || misaligned(weight, 4) ||
         misaligned(loss, 4) || misaligned(dH, 16) || misaligned(workspace, 256) || workspace_bytes < L.bytes)
         return LB_ERR_INVALID_ARG;
-    const size_t tiles_n = L.ntn, tiles_d = (D + kMmTile - 1) / kMmTile, tiles_m = (L.rows + kMmTile - 1) / kMmTile;
-    if (tiles_m * tiles_n > (1u << 28) || tiles_n * tiles_d > (1u << 28) || tiles_m * tiles_d * L.splits > (1u << 28))
-        return LB_ERR_UNSUPPORTED;
     if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
     unsigned char *ws = (unsigned char *)workspace;
     int launches = 1;

@@ -1468,6 +1468,10 @@ bool orth_shapes_ok(const int *rows, const int *cols, int n)
         if (rows[i] < 1 || cols[i] < 1) return false;
     return true;
 }
+bool orth_supported(int rows, int cols)
+{
+    return std::min(rows, cols) <= LB_MAX_RANK && std::max(rows, cols) <= (1 << 24);
+}
 
 }  // namespace
 
@@ -1480,6 +1484,8 @@ using namespace lb;
 extern "C" size_t lb_orthogonalise_workspace_bytes(const int *rows, const int *cols, int n, int dtype)
 {
     if (!orth_shapes_ok(rows, cols, n) || (dtype != LB_F32 && dtype != LB_BF16)) return 0;
+    for (int i = 0; i < n; ++i)
+        if (!orth_supported(rows[i], cols[i])) return 0;
     try {
         std::vector<Chunk> chunks;
         orth_chunks(chunks, rows, cols, n, dtype == LB_BF16);
@@ -1503,7 +1509,7 @@ extern "C" lb_status lb_orthogonalise(const void *const *G, int dtype, const int
     if (!G || !O || !workspace || misaligned(workspace, 256)) return LB_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
         if (!G[i] || !O[i] || misaligned(G[i], dtype == LB_F32 ? 4 : 2) || misaligned(O[i], 2)) return LB_ERR_INVALID_ARG;
-        if (std::min(rows[i], cols[i]) > LB_MAX_RANK || std::max(rows[i], cols[i]) > (1 << 24)) return LB_ERR_UNSUPPORTED;
+        if (!orth_supported(rows[i], cols[i])) return LB_ERR_UNSUPPORTED;
     }
     try {
         std::vector<Chunk> chunks;

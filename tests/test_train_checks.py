@@ -200,3 +200,30 @@ int main(void)
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "OK", (r.returncode, r.stdout, r.stderr)
+
+
+def test_workspace_sizes_of_refused_shapes(lib):
+    """A size that the call refuses has no scratch: the query answers 0, at once."""
+    f32, bf = torch.float32, torch.bfloat16
+    for dtype in (f32, bf):
+        for bad in ((2049, 2049), (300000, 300000), (2 ** 31 - 1, 2 ** 31 - 1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1)):
+            assert lib.lb_orthogonalise_workspace_bytes([(300, 100), bad], dtype) == 0, bad
+        assert lib.lb_orthogonalise_workspace_bytes([(2048, 2048), (1 << 24, 100)], dtype) > 0
+    assert lib.lb_embedding_backward_workspace_bytes(4, 10, 1 << 23) > 0
+    assert lib.lb_embedding_backward_workspace_bytes(4, 10, (1 << 23) + 1) == 0
+    assert lib.lb_embedding_backward_workspace_bytes(1 << 31, 10, 8) == 0
+    for query in (lib.lb_cross_entropy_forward_workspace_bytes, lib.lb_cross_entropy_gradient_workspace_bytes):
+        assert query(4, 64, 100) > 0
+        for bad in ((4, 60, 100), (-1, 64, 100), (4, (1 << 20) + 8, 100), (4, 64, (1 << 28) + 1), ((1 << 28) + 1, 64, 100)):
+            assert query(*bad) == 0, bad
+
+
+@pytest.mark.gpu
+def test_refused_ranks_take_no_scratch(lib):
+    G = torch.zeros(3000, 2500, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(lib.LittleBitError, match="UNSUPPORTED"):
+        lib.lb_orthogonalise([G])
+    assert torch.cuda.max_memory_allocated() - before <= G.numel() * 2 + 4096         # the output alone
