@@ -587,6 +587,13 @@ def _sizes(names: str, *sizes):
             raise ValueError(f"{name} must be 0 .. 2^31 - 1, got {n}")
 
 
+def _fit(names: str, *numbers):
+    """The same for numbers whose range the library checks by itself."""
+    for name, n in zip(names.split(), numbers):
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {n}")
+
+
 def _workspace(workspace, need: int, on: _On) -> torch.Tensor:
     if workspace is None:
         return torch.empty(max(need, 1), dtype=torch.uint8, device=on.device)
@@ -628,7 +635,8 @@ def lb_embedding_forward(ids: torch.Tensor, table: torch.Tensor, scale: float = 
 
 
 def lb_embedding_backward_workspace_bytes(M: int, V: int, D: int) -> int:
-    return int(_lib.lb_embedding_backward_workspace_bytes(M, V, D))
+    _fit("V D", V, D)
+    return int(_lib.lb_embedding_backward_workspace_bytes(min(M, 1 << 62), V, D))   # 0 from 2^31 on
 
 
 def lb_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, scale: float = 1.0,
@@ -651,10 +659,12 @@ def lb_embedding_backward(ids: torch.Tensor, dout: torch.Tensor, V: int, scale: 
 
 
 def lb_cross_entropy_forward_workspace_bytes(M: int, D: int, V: int) -> int:
+    _fit("M D V", M, D, V)
     return int(_lib.lb_cross_entropy_forward_workspace_bytes(M, D, V))
 
 
 def lb_cross_entropy_gradient_workspace_bytes(M: int, D: int, V: int, head: bool = True, rows: int = 0) -> int:
+    _fit("M D V rows", M, D, V, rows)
     return int(_lib.lb_cross_entropy_gradient_workspace_bytes(M, D, V, int(head), rows))
 
 
@@ -705,6 +715,8 @@ def lb_cross_entropy_gradient(H: torch.Tensor, W: torch.Tensor, labels: torch.Te
 
 def lb_orthogonalise_workspace_bytes(shapes, dtype: torch.dtype = torch.float32) -> int:
     n = len(shapes)
+    for shape in shapes:
+        _fit("rows cols", *shape)
     rows, cols = ((_i * max(1, n))(*[s[k] for s in shapes]) for k in (0, 1))
     return int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, _element(dtype, "dtype")))
 
@@ -739,6 +751,8 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
             raise ValueError(f"G[{i}] must be a matrix with at least one element")
         if max(shape) >= 1 << 31:
             raise ValueError(f"G[{i}] has a side of {max(shape)}, 2^31 - 1 at most")
+    steps = int(steps)
+    _fit("steps", steps)
     dtype, names = G[0].dtype, _Names("G")
     code = _element(dtype, "G")
     ints, ptrs = _array(_i, n), _array(_vp, n)
@@ -748,6 +762,6 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
                      for i, t in enumerate(G)])
         out = _outputs(G, shapes)
         ws = _workspace(workspace, int(_lib.lb_orthogonalise_workspace_bytes(rows, cols, n, code)), on)
-        _check(_lib.lb_orthogonalise(src, code, rows, cols, n, int(steps), float(eps), ptrs(*[t.data_ptr() for t in out]),
+        _check(_lib.lb_orthogonalise(src, code, rows, cols, n, steps, float(eps), ptrs(*[t.data_ptr() for t in out]),
                                      _dev(ws, torch.uint8, "workspace"), ws.numel(), on.stream), "lb_orthogonalise")
     return out

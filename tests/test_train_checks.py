@@ -227,3 +227,27 @@ def test_refused_ranks_take_no_scratch(lib):
     with pytest.raises(lib.LittleBitError, match="UNSUPPORTED"):
         lib.lb_orthogonalise([G])
     assert torch.cuda.max_memory_allocated() - before <= G.numel() * 2 + 4096         # the output alone
+
+
+def test_workspace_sizes_refuse_past_a_c_int(lib):
+    """A number that ctypes would cut to 32 bits, in every argument of the size functions, and of the call's own steps."""
+    huge = (1 << 32) + 4
+    for k in range(1, 3):
+        args = [4, 10, 8]
+        args[k] = huge
+        with pytest.raises(ValueError, match="fit"):
+            lib.lb_embedding_backward_workspace_bytes(*args)
+    assert lib.lb_embedding_backward_workspace_bytes((1 << 64) + 4, 10, 8) == 0
+    for query, n in ((lib.lb_cross_entropy_forward_workspace_bytes, 3), (lib.lb_cross_entropy_gradient_workspace_bytes, 5)):
+        for k in range(n):
+            args = [4, 8, 10, True, 0][:n]
+            if k == 3:
+                continue
+            args[k] = huge
+            with pytest.raises(ValueError, match="fit"):
+                query(*args)
+    for bad in ((huge, 16), (16, huge)):
+        with pytest.raises(ValueError, match="fit"):
+            lib.lb_orthogonalise_workspace_bytes([(16, 16), bad])
+    with pytest.raises(ValueError, match="steps must fit"):
+        lib.lb_orthogonalise([torch.zeros(3, 4)], steps=(1 << 32) + 5)
