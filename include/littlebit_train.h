@@ -17,12 +17,12 @@
  * call here allocates device memory or keeps anything between calls: scratch
  * is the `workspace` argument, 256-byte aligned and at least as large as the
  * matching *_workspace_bytes call says (host only; 0 also for sizes that the
- * operator refuses); its contents need not be initialised and mean nothing
- * afterwards.  Calls that use different workspaces and
- * outputs may overlap on the device (streams, captured graphs); calls that
- * share one must be ordered.  All calls can be captured into a CUDA graph.
- * Outputs must not overlap inputs.  The same call gives the same bits every
- * time.
+ * operator refuses; NULL will do where 0 bytes are needed); its contents need
+ * not be initialised and mean nothing afterwards.  Calls that use different
+ * workspaces and outputs may overlap on the device (streams, captured graphs);
+ * calls that share one must be ordered.  All calls can be captured into a CUDA
+ * graph.
+ * Outputs must not overlap inputs.  The same call gives the same bits every time.
  */
 #ifndef LITTLEBIT_TRAIN_H
 #define LITTLEBIT_TRAIN_H

@@ -1506,7 +1506,7 @@ extern "C" lb_status lb_orthogonalise(const void *const *G, int dtype, const int
         return LB_ERR_INVALID_ARG;
     if (steps > kMaxSteps) return LB_ERR_UNSUPPORTED;
     if (n == 0) return LB_OK;
-    if (!G || !O || !workspace || misaligned(workspace, 256)) return LB_ERR_INVALID_ARG;
+    if (!G || !O) return LB_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
         if (!G[i] || !O[i] || misaligned(G[i], dtype == LB_F32 ? 4 : 2) || misaligned(O[i], 2)) return LB_ERR_INVALID_ARG;
         if (!orth_supported(rows[i], cols[i])) return LB_ERR_UNSUPPORTED;
@@ -1515,7 +1515,7 @@ extern "C" lb_status lb_orthogonalise(const void *const *G, int dtype, const int
         std::vector<Chunk> chunks;
         orth_chunks(chunks, rows, cols, n, dtype == LB_BF16);
         for (const Chunk &c : chunks)
-            if (workspace_bytes < c.bytes) return LB_ERR_INVALID_ARG;
+            if (c.bytes && (!workspace || misaligned(workspace, 256) || workspace_bytes < c.bytes)) return LB_ERR_INVALID_ARG;
         if (tmap_encoder_ready() != cudaSuccess) return LB_ERR_UNSUPPORTED;
         int launches = 0;
         for (const Chunk &c : chunks) {

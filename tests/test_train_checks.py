@@ -251,3 +251,14 @@ def test_workspace_sizes_refuse_past_a_c_int(lib):
             lib.lb_orthogonalise_workspace_bytes([(16, 16), bad])
     with pytest.raises(ValueError, match="steps must fit"):
         lib.lb_orthogonalise([torch.zeros(3, 4)], steps=(1 << 32) + 5)
+
+
+@pytest.mark.gpu
+def test_no_workspace_where_none_is_needed(lib):
+    i = ctypes.c_int
+    G = torch.randn(512, 16, device="cuda")
+    O = torch.empty(512, 16, dtype=torch.bfloat16, device="cuda")
+    assert lib.lb_orthogonalise_workspace_bytes([(512, 16)]) == 0
+    st = lib._lib.lb_orthogonalise((vp * 1)(G.data_ptr()), 0, (i * 1)(512), (i * 1)(16), 1, 5, 1e-7, (vp * 1)(O.data_ptr()),
+                                   None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == OK and torch.equal(O, lib.lb_orthogonalise([G])[0])
