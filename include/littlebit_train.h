@@ -12,9 +12,10 @@
  *
  * Conventions are those of littlebit.h: device pointers unless stated, arrays
  * of pointers are HOST arrays of device pointers, row-major dense matrices,
- * `stream` is a cudaStream_t passed as void*, every check is made before
- * anything is enqueued, nothing synchronises the host unless it says so.  No
- * call here allocates device memory or keeps anything between calls: scratch
+ * `stream` is a cudaStream_t passed as void*, every check of the arguments is
+ * made before anything is enqueued (LB_ERR_CUDA and LB_ERR_OOM can come later and
+ * leave the outputs unspecified), nothing synchronises the host unless it says
+ * so.  No call here allocates device memory or keeps anything between calls: scratch
  * is the `workspace` argument, 256-byte aligned and at least as large as the
  * matching *_workspace_bytes call says (host only; 0 also for sizes that the
  * operator refuses; NULL will do where 0 bytes are needed); its contents need
@@ -92,7 +93,7 @@ LB_API lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t *W, 
  *
  *   weight  float32 [M]       loss  float32 [M]
  *   dH      bfloat16 [M][D]   dW    bfloat16 [V][D], or NULL for a frozen vocabulary matrix; both are overwritten
- *   rows    rows taken at a time (0: 8192; at most 32768).  The scratch holds 16 bits per
+ *   rows    rows taken at a time (0: 8192; more than 32768: 32768).  The scratch holds 16 bits per
  *           logit of one such piece, never of all M rows when M is larger;
  *           with more than one piece dW is summed over them in float32.
  * G is rounded to bfloat16 once, as an operand of the two products; they

@@ -595,7 +595,7 @@ lb_status few_logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, in
         !mm_operand(&G.mB[0], true, false, H, M, D, D, 1, width / 2) ||
         !tmap_encode_3d(&E.mD, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.part, L.Mp, V, L.ranges, (long)L.Mp * 4,
                         (long)V * L.Mp * 4, 32, 32))
-        return LB_ERR_INVALID_ARG;
+        return LB_ERR_CUDA;
     return status_from(mm_launch<true, 1, FewEpi>(G, E, s));
 }
 
@@ -609,7 +609,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
     mm_chunk(G.p[0], kChunk);
     G.nunits = mm_units(G.p[0]);
     if (!mm_operand(&G.mA[0], true, false, H, M, D, D) || !mm_operand(&G.mB[0], true, false, W, V, D, D))
-        return LB_ERR_INVALID_ARG;
+        return LB_ERR_CUDA;
     auto fill = [&](auto &E) {
         memset(&E, 0, sizeof(E));
         E.labels = labels;
@@ -623,7 +623,7 @@ lb_status logits(const LossPlan &L, const uint16_t *H, const uint16_t *W, const 
         LogitEpi<true>::Params E;
         fill(E);
         if (!tmap_encode_2d(&E.mE, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + L.E, L.Vp, M, (long)L.Vp * 2, 64, 32))
-            return LB_ERR_INVALID_ARG;
+            return LB_ERR_CUDA;
         return status_from(mm_launch<true, 1, LogitEpi<true>>(G, E, s));
     }
     LogitEpi<false>::Params E;
@@ -646,7 +646,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
     mm_chunk(P, kChunk);
     P.b_mn = 1;
     if (!mm_operand(&G.mA[0], true, false, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[0], true, true, W, V, D, D))
-        return LB_ERR_INVALID_ARG;
+        return LB_ERR_CUDA;
     const int tile_rows = P.ntm * kMmTile;
     bool ok;
     if (P.splits > 1) {
@@ -658,7 +658,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
         E.kind[0] = kOutBf16;
         ok = tmap_encode_2d(&E.mD[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dH, D, M, (long)D * 2, 64, 32);
     }
-    if (!ok) return LB_ERR_INVALID_ARG;
+    if (!ok) return LB_ERR_CUDA;
     G.n = 1;
     G.nunits = mm_units(P);
     if (dW) {
@@ -667,7 +667,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
         mm_chunk(Q, kChunk);
         Q.a_mn = Q.b_mn = 1;
         if (!mm_operand(&G.mA[1], true, true, Gm, M, L.Vp, L.Vp) || !mm_operand(&G.mB[1], true, true, ws + L.Hc, M, D, D))
-            return LB_ERR_INVALID_ARG;
+            return LB_ERR_CUDA;
         if (L.npieces > 1) {
             E.kind[1] = first ? kOutF32 : kOutF32Add;
             ok = tmap_encode_2d(&E.mD[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, ws + L.acc, D, V, (long)D * 4, 32, 32);
@@ -675,7 +675,7 @@ lb_status products(const LossPlan &L, const uint16_t *W, int M, int D, int V, ui
             E.kind[1] = kOutBf16;
             ok = tmap_encode_2d(&E.mD[1], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, D, V, (long)D * 2, 64, 32);
         }
-        if (!ok) return LB_ERR_INVALID_ARG;
+        if (!ok) return LB_ERR_CUDA;
         int pairs = 0;
         const cudaError_t e = mm_pairs(&pairs);
         if (e != cudaSuccess) return status_from(e);

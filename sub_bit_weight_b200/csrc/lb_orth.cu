@@ -1306,7 +1306,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         ++R.n;
     }
     mm_deal(R.order, R.p, R.n, R.nunits, pairs);
-    if (!ok) return LB_ERR_INVALID_ARG;
+    if (!ok) return LB_ERR_CUDA;
     ++*launches;
     if ((e = mm_launch<false, kMostGroups, GramEpi>(R, D, s)) != cudaSuccess) return status_from(e);
 
@@ -1384,7 +1384,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
             }
         }
         deal(one);
-        if (!ok) return LB_ERR_INVALID_ARG;
+        if (!ok) return LB_ERR_CUDA;
         if ((e = launch()) != cudaSuccess) return status_from(e);
         if (k + 1 == steps && k == 0) break;
         begin();   // T = a A + A p, and Q <- a Q + Q p
@@ -1398,14 +1398,14 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
             }
         }
         deal(k && k + 1 < steps ? two : one);
-        if (!ok) return LB_ERR_INVALID_ARG;
+        if (!ok) return LB_ERR_CUDA;
         if ((e = launch()) != cudaSuccess) return status_from(e);
         if (k + 1 == steps) break;
         begin();   // A <- a T + T p
         for (const Group &g : C.groups)
             if (g.n > kMidN) square(g, g.T, g.q, g.A, 1.0f / kSA, kA, g.T);
         deal(one);
-        if (!ok) return LB_ERR_INVALID_ARG;
+        if (!ok) return LB_ERR_CUDA;
         if ((e = launch()) != cudaSuccess) return status_from(e);
     }
 
@@ -1434,7 +1434,7 @@ lb_status orth_chunk(const Chunk &C, const void *const *Gs, bool bf16, int steps
         ++B.n;
     }
     mm_deal(B.order, B.p, B.n, B.nunits, pairs);
-    if (!ok) return LB_ERR_INVALID_ARG;
+    if (!ok) return LB_ERR_CUDA;
     if ((e = launch()) != cudaSuccess) return status_from(e);
     return status_from(cudaGetLastError());
 }
