@@ -60,6 +60,7 @@
 #include <vector>
 
 #include "lb_mm.cuh"
+#include "lb_orth_index.h"
 #include "littlebit_train.h"
 
 namespace lb {
@@ -186,23 +187,20 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Mats
     }
     __syncthreads();
     const float c = sc;
-    const int nv = m.pitch / 8;
-    const size_t plane = (size_t)m.rows * m.pitch, total = (size_t)m.rows * nv;
+    const size_t plane = (size_t)m.rows * m.pitch, total = plane / 8;
     const bool wide_loads = !P.bf16 && m.cols % 4 == 0 && ((uintptr_t)m.G & 15) == 0;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)m.nblocks * 256) {
-        const size_t row = i / nv;
-        const int col = (int)(i - row * nv) * 8;
-        const size_t g = row * m.cols + col;
+        const SplitVector e = split_vector(i, m.cols, m.pitch);
         float x[8];
-        if (wide_loads) {
-            const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(m.G) + g);
+        if (wide_loads) {   // e.n is 0, 4 or 8
+            const float4 *src = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(m.G) + e.at);
             const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const float4 u = col < m.cols ? src[0] : zero, v = col + 4 < m.cols ? src[1] : zero;
+            const float4 u = e.n >= 4 ? src[0] : zero, v = e.n == 8 ? src[1] : zero;
             x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
             x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = col + j < m.cols ? load_g(m.G, g + j, P.bf16) : 0.0f;
+            for (int j = 0; j < 8; ++j) x[j] = j < e.n ? load_g(m.G, e.at + j, P.bf16) : 0.0f;
         }
         alignas(16) __half hi[8], lo[8];
 #pragma unroll
