@@ -89,3 +89,25 @@ def test_cross_entropy_gradient_of_the_vocabulary_over_many_rows(lib):  # noqa: 
     mags = torch.stack([G[m:m + 1024].T.abs() @ Hd[m:m + 1024] for m in range(0, M, 1024)])
     bound = 64 * MMA * mags.sum(0) + len(mags) * 2.0 ** -24 * 200.0
     _within(dW, ref, bound + 2.0 ** -8 * (ref.abs() + bound))
+
+
+@pytest.mark.parametrize("M,D,rows", [(300, 264, 0), (5, 1032, 0), (700, 520, 256), (2, 8, 0)])
+def test_cross_entropy_gradient_of_hidden_states_keeps_the_label_entry(lib, M, D, rows):  # noqa: F811
+    """p - 1 = -511/512 lies halfway between two bfloat16 numbers; rounded, it would scale each row's part of W[label] by
+    2^-9 of it, the same way in every column.  All else is exact (p = 2^-9), so the result is within the accumulation's
+    errors of half a step of itself: 64 additions of 2^-22 of the magnitudes, and a float32 rounding or two."""
+    V = 512
+    g = _gen(M)
+    W = torch.randn(V, D, generator=g, device="cuda").to(BF16)
+    H = torch.zeros(M, D, dtype=BF16, device="cuda")
+    labels = torch.randint(0, V, (M,), generator=g, device="cuda")
+    labels[1::3] = -100
+    weight = torch.where(torch.arange(M, device="cuda") % 2 == 0, 1.0, 0.25)
+    _, dH, _ = lib.lb_cross_entropy_gradient(H, W, labels, weight, rows=rows)
+    ok = (labels >= 0)[:, None]
+    Wd = W.double()
+    w = weight.double()[:, None] * ok
+    ref = w * (Wd.sum(0) / V - Wd[labels.clamp(min=0)])
+    e = w * 65 * MMA * (Wd.abs().sum(0) / V + Wd[labels.clamp(min=0)].abs())
+    half_step = torch.exp2(torch.floor(torch.log2((ref.abs() + e).clamp(min=1e-30))) - 8)
+    _within(dH, ref, torch.where(ok, e + half_step, 0.0))
