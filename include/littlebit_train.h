@@ -96,6 +96,8 @@ LB_API lb_status lb_cross_entropy_forward(const uint16_t *H, const uint16_t *W, 
  *   rows    rows taken at a time (0: 8192; more than 32768: 32768).  The scratch holds 16 bits per
  *           logit of one such piece, never of all M rows when M is larger;
  *           with more than one piece dW is summed over them in float32.
+ * Softmax entries go through binary16 relative to the largest of their 128
+ * neighbours (v / 128): right to 2^-11, but 0 below 2^-40 of that one.
  * G is rounded to bfloat16 once, as an operand of the two products (dH is made
  * good for the rounding of the label's entry); they accumulate in float32 and
  * dH, dW are rounded once.  All else as above; rows

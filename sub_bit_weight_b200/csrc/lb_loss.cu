@@ -11,8 +11,9 @@
 //   1  z tiles (256 rows x 256 vocabulary entries) on CTA pairs.  The epilogue
 //      takes each row's maximum m and sum of exp(z - m) over the tile (one
 //      thread a row and 128 columns, which it holds in registers) and, for the gradient,
-//      leaves e = 2^15 exp(z - m) in binary16: at most 2^15, exact to 2^-12
-//      down to 2^-29 of the tile's maximum and to 2^-39 of it below that.
+//      leaves e = 2^15 exp(z - m) in binary16: at most 2^15, right to 2^-11
+//      down to 2^-29 of the maximum of those columns and to 2^-40 of that
+//      maximum below (so less than that is 0).
 //   2  one block per row and 8192 entries: lse from the tiles' (m, s), then
 //      G / max w = w / max w (e exp(m - lse) 2^-15 - onehot), rounded to
 //      bfloat16, over e, and what this rounding left of the label's entry.

@@ -18,7 +18,7 @@
 //
 // Precision.  The small singular values of an update are what the iteration
 // blows up (by up to a^steps = 485), and in A_0 they are squared, so an error
-// of 2^-12 in A (one binary16 rounding) would move them by percents.  Every
+// of 2^-11 in A (one binary16 rounding) would move them by percents.  Every
 // operand is therefore a pair of binary16 halves, hi + lo, 22 bits, and a
 // product is hi hi + lo hi + hi lo in one float32 accumulator for each k block,
 // whose halves are copied once for the three.  p is kept rather than q, whose
