@@ -398,8 +398,10 @@ struct ProductEpi {
         int split_rows[2];   // rows between the partial results of consecutive k ranges
         const float *wref;
         // What the rounding of G left of each row's label entry, up to 2^-9: by itself more than the other entries' roundings
-        // together, and a multiple of W[label] in dH's row, so it is made up for there: dH += rest W[label] (1.91e-3 ->
-        // 1.66e-3 of the norm, which is the rounding of the result, at 4096 rows, D 4096, V 32000).  This takes 2 to 5 us of a call of few rows (205 -> 208 us at 1 row, D 4096, V 32000) and nothing measurable of larger ones.
+        // together where none of them is large, and a multiple of W[label] in dH's row, so it is made up for there:
+        // dH += rest W[label] (1.91e-3 -> 1.66e-3 of the norm, which is the rounding of the result, at 4096 rows, D 4096,
+        // V 32000).  This takes 2 to 5 us of a call of few rows (205 -> 208 us at 1 row, D 4096, V 32000), and about 1 % of
+        // larger ones together with the pieces.
         const float *rest;
         const int64_t *labels;
         const uint16_t *W;
@@ -829,8 +831,8 @@ extern "C" lb_status lb_cross_entropy_gradient(const uint16_t *H, const uint16_t
         cudaError_t e = launch_after(grad_kernel, grid, 256, s, (uint4 *)(ws + L.E), (const float2 *)(ws + L.stat),
                                          (const float *)(ws + L.target), labels + r0, weight + r0,
                                          (const float *)(ws + L.wref), V, L.Vp, L.nst, D,
-                                         (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0, (float *)(ws + L.rest),
-                                         cols);
+                                         (const uint4 *)Hp, dW ? (uint4 *)(ws + L.Hc) : nullptr, loss + r0,
+                                         (float *)(ws + L.rest), cols);
         if (e != cudaSuccess) return status_from(e);
         launches += 2;
         st = products(L, W, labels + r0, m, D, V, dH + (size_t)r0 * D, dW, p == 0, ws, s, &launches);
