@@ -752,7 +752,8 @@ def lb_orthogonalise(G, steps: int = 5, eps: float = 1e-7, workspace: torch.Tens
         if max(shape) >= 1 << 31:
             raise ValueError(f"G[{i}] has a side of {max(shape)}, 2^31 - 1 at most")
     steps = int(steps)
-    _fit("steps", steps)
+    if not 0 < steps < 16:   # outside the usual ones; the check takes as long as a few tensors' marshalling
+        _fit("steps", steps)
     dtype, names = G[0].dtype, _Names("G")
     code = _element(dtype, "G")
     ints, ptrs = _array(_i, n), _array(_vp, n)
